@@ -327,6 +327,84 @@ size_t awq_gptq_factor_workspace_size(int64_t in);
 size_t awq_gptq_quantize_workspace_size(int64_t out, int64_t in);
 size_t awq_gptq_workspace_size(int64_t out, int64_t in);
 
+/* Microscaled 4-bit floating point (MXFP4): every block of AWQ_MX4_BLOCK = 32
+ * consecutive columns of a row shares a power of two, and a value is one of
+ * +-{0, 0.5, 1, 1.5, 2, 3, 4, 6} times it. The form that gfx950's scaled matrix
+ * instructions take directly, for weights and for activations.
+ *   codes:  device uint8 (rows, in / 2): column 2i in the low half of byte i of
+ *           the row, column 2i + 1 in the high half; a code's bit 3 is the sign,
+ *           bits 0-2 index the magnitudes above.
+ *   scales: device uint8 (rows, in / 32): byte b stands for 2^(b - 127), 255 for
+ *           NaN (every value of its block is NaN, whatever the codes).
+ * `in` must be a multiple of 32. 4.25 bits per value.
+ *
+ * awq_mx4_quantize: with v = fp32(W[r, j] * s[j]) (s NULL: v = fp32(W[r, j]))
+ * and A the largest |v| of a block, e = clamp(floor(log2 A) - 2, -127, 127) (A = 0:
+ * -127), byte = e + 127; a code has v's sign and |v| * 2^-e rounded to the
+ * nearest magnitude, ties to the even code, 6 above 6. Bit-exact. A block with
+ * an infinity or a NaN gets byte 255 and codes 0.
+ *   W: device (rows, in) of `dtype`, 16-byte aligned; e.g. a layer's weights
+ *      (s: device fp32[in], 16-byte aligned, as s_best of awq_search, or NULL),
+ *      several layers' or experts' stacked, or activations.
+ * awq_mx4_dequantize: out (rows, in) of `dtype` = the values, rounded to nearest
+ * even where `dtype` does not hold them (bf16 and fp32 hold all below 2^128).
+ * AWQ_ERR_UNSUPPORTED: W, s, codes or out not 16-byte aligned, or a matrix of
+ * more than 2^43 values. */
+#define AWQ_MX4_BLOCK 32
+int awq_mx4_quantize(const void *W, int dtype, int64_t rows, int64_t in, const float *s, uint8_t *codes,
+                     uint8_t *scales, void *stream);
+int awq_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t in, void *out,
+                       int dtype, void *stream);
+
+/* The deployment products over MXFP4 weights W (out, in):
+ *   awq_mx4_gemm:    Y[m][n] = sum_k X[m][k] * W[n][k], X (M, in) of x_dtype
+ *                    (AWQ_F16 or AWQ_BF16); Y of y_dtype: AWQ_F32 or x_dtype.
+ *   awq_mx4_gemm_a4: the same with X MXFP4 too (as awq_mx4_quantize writes it);
+ *                    Y of y_dtype, any.
+ * Operands enter the matrix cores without rounding and are summed in fp32 in a
+ * fixed order (bitwise reproducible): each output is within
+ * (in + 16) * 2^-24 * sum_k |X[m][k] W[n][k]| of the exact value, plus the
+ * rounding to a 16-bit Y. A row of X or W that holds a NaN makes its own
+ * outputs NaN and no others.
+ * AWQ_ERR_UNSUPPORTED: x_dtype AWQ_F32, X or codes (xcodes) not 16-byte aligned,
+ * M above 2 097 120, or `in` above 2^30. */
+int awq_mx4_gemm(const void *X, int x_dtype, int64_t M, int64_t in, const uint8_t *codes,
+                 const uint8_t *scales, int64_t out, void *Y, int y_dtype, void *stream);
+int awq_mx4_gemm_a4(const uint8_t *xcodes, const uint8_t *xscales, int64_t M, int64_t in,
+                    const uint8_t *codes, const uint8_t *scales, int64_t out, void *Y, int y_dtype,
+                    void *stream);
+
+/* A mixture-of-experts layer for a few tokens (decoding), experts in MXFP4. For
+ * each token x (a row of X):
+ *   l = router x (fp32); the top_k experts with the largest l (equal ones: the
+ *   lowest index; a NaN ranks lowest); p = softmax(l) over all experts at those,
+ *   divided by their sum if renorm is not 0;
+ *   h_e = silu(Wgate_e x) * (Wup_e x);  y = sum_e p_e Wdown_e h_e.
+ * p_e h_e is rounded once to `dtype`, the type in which the layer's matrix
+ * products take their activations; everything else is fp32 up to Y.
+ *   X:      device (M, hidden) of `dtype` (AWQ_F16 or AWQ_BF16), M <= AWQ_MX4_MOE_MAX_TOKENS.
+ *   router: device (experts, hidden) of `dtype`.
+ *   gu_codes, gu_scales: device, the MXFP4 matrix (experts * 2 * inter, hidden): of each
+ *           expert the inter gate rows, then the inter up rows.
+ *   dn_codes, dn_scales: device, the MXFP4 matrix (experts * hidden, inter).
+ *   Y:      device (M, hidden) of `dtype` (output); must not overlap an input.
+ *   ws:     device scratch of awq_mx4_moe_workspace_size(M, inter, top_k) bytes
+ *           (0 for sizes that the call refuses). Calls that overlap in time need
+ *           a workspace each.
+ * hidden and inter must be multiples of 32, 1 <= top_k <= experts.
+ * An expert's NaN or infinite values reach only the tokens routed to it.
+ * AWQ_ERR_UNSUPPORTED: dtype AWQ_F32, M > AWQ_MX4_MOE_MAX_TOKENS, top_k >
+ * AWQ_MX4_MOE_MAX_TOPK, experts > AWQ_MX4_MOE_MAX_EXPERTS, hidden or inter above
+ * 2^20, X, router, codes or ws not 16-byte aligned. */
+#define AWQ_MX4_MOE_MAX_TOKENS 64
+#define AWQ_MX4_MOE_MAX_TOPK 16
+#define AWQ_MX4_MOE_MAX_EXPERTS 256
+int awq_mx4_moe(const void *X, int dtype, int64_t M, int64_t hidden, int64_t inter, int experts, int top_k,
+                int renorm, const void *router, const uint8_t *gu_codes, const uint8_t *gu_scales,
+                const uint8_t *dn_codes, const uint8_t *dn_scales, void *Y, void *ws, size_t ws_bytes,
+                void *stream);
+size_t awq_mx4_moe_workspace_size(int64_t M, int64_t inter, int top_k);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char *awq_status_string(int status);
 

@@ -92,6 +92,19 @@ def lib():
         for fn in ("awq_gptq_quantize_workspace_size", "awq_gptq_workspace_size"):
             getattr(L, fn).argtypes = [i64, i64]
             getattr(L, fn).restype = sz
+        u8 = vp
+        L.awq_mx4_quantize.argtypes = [vp, cint, i64, i64, vp, u8, u8, vp]
+        L.awq_mx4_quantize.restype = cint
+        L.awq_mx4_dequantize.argtypes = [u8, u8, i64, i64, vp, cint, vp]
+        L.awq_mx4_dequantize.restype = cint
+        L.awq_mx4_gemm.argtypes = [vp, cint, i64, i64, u8, u8, i64, vp, cint, vp]
+        L.awq_mx4_gemm.restype = cint
+        L.awq_mx4_gemm_a4.argtypes = [u8, u8, i64, i64, u8, u8, i64, vp, cint, vp]
+        L.awq_mx4_gemm_a4.restype = cint
+        L.awq_mx4_moe.argtypes = [vp, cint, i64, i64, i64, cint, cint, cint, vp, u8, u8, u8, u8, vp, vp, sz, vp]
+        L.awq_mx4_moe.restype = cint
+        L.awq_mx4_moe_workspace_size.argtypes = [i64, i64, cint]
+        L.awq_mx4_moe_workspace_size.restype = sz
         L.awq_status_string.argtypes = [cint]
         L.awq_status_string.restype = ctypes.c_char_p
         _lib = L
@@ -359,6 +372,126 @@ def qgemm(X, qweight, scales, zeros, bits, group, y=None, y_f32=False):
         _dev(X, "X"), _dtype_code(X), M, n_in, _dev(qweight, "qweight"),
         _dev(scales, "scales", torch.float32), _dev(zeros, "zeros", torch.uint8), out, bits, group,
         _dev(y, "y", ydt), _DTYPE[ydt], _stream()))
+    return y
+
+
+MX4_BLOCK = 32                     # columns that share an MXFP4 scale
+MX4_MOE_MAX_TOKENS, MX4_MOE_MAX_TOPK, MX4_MOE_MAX_EXPERTS = 64, 16, 256
+
+
+def _launch(name, device, *args):
+    """Calls the library on `device` and the stream that is current there."""
+    if device.index == torch.cuda.current_device():
+        _check(name, getattr(lib(), name)(*args, _stream()))
+    else:
+        with torch.cuda.device(device):
+            _check(name, getattr(lib(), name)(*args, _stream()))
+
+
+def _on(device, t, name, dtype=None):
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    return _dev(t, name, dtype)
+
+
+def _mx4_cols(codes, scales, what=""):
+    """Columns of an MXFP4 matrix (codes uint8 (..., in / 2), scales uint8 (..., in / 32))."""
+    if codes.dim() < 2 or scales.dim() != codes.dim() or codes.shape[:-1] != scales.shape[:-1] \
+            or codes.shape[-1] * 2 != scales.shape[-1] * MX4_BLOCK:
+        raise ValueError(f"{what}codes must be (..., in / 2) and {what}scales (..., in / {MX4_BLOCK})")
+    return codes.shape[-1] * 2
+
+
+def mx4_quantize(W, s=None, codes=None, scales=None):
+    """W (..., in) to MXFP4 along its last dimension: (codes uint8 (..., in / 2),
+    scales uint8 (..., in / 32)); with `s` (fp32 [in]) of W diag(s)."""
+    if W.dim() < 2 or W.shape[-1] % MX4_BLOCK != 0:
+        raise ValueError(f"W must be (..., in) with in a multiple of {MX4_BLOCK}")
+    n_in = W.shape[-1]
+    if codes is None:
+        codes = torch.empty(W.shape[:-1] + (n_in // 2,), dtype=torch.uint8, device=W.device)
+    if scales is None:
+        scales = torch.empty(W.shape[:-1] + (n_in // MX4_BLOCK,), dtype=torch.uint8, device=W.device)
+    _need(codes, "codes", W.shape[:-1] + (n_in // 2,))
+    _need(scales, "scales", W.shape[:-1] + (n_in // MX4_BLOCK,))
+    if s is not None:
+        _need(s, "s", (n_in,))
+    dev = W.device
+    _launch("awq_mx4_quantize", dev, _dev(W, "W"), _dtype_code(W), W.numel() // max(n_in, 1), n_in,
+            None if s is None else _on(dev, s, "s", torch.float32), _on(dev, codes, "codes", torch.uint8),
+            _on(dev, scales, "scales", torch.uint8))
+    return codes, scales
+
+
+def mx4_dequantize(codes, scales, dtype=torch.bfloat16, out=None):
+    """The values (..., in) that MXFP4 codes and scales stand for, as `dtype`."""
+    n_in = _mx4_cols(codes, scales)
+    shape = codes.shape[:-1] + (n_in,)
+    out = torch.empty(shape, dtype=dtype, device=codes.device) if out is None else out
+    _need(out, "out", shape)
+    dev = codes.device
+    _launch("awq_mx4_dequantize", dev, _dev(codes, "codes", torch.uint8), _on(dev, scales, "scales", torch.uint8),
+            out.numel() // max(n_in, 1), n_in, _on(dev, out, "out"), _dtype_code(out))
+    return out
+
+
+def mx4_gemm(X, codes, scales, y=None, y_f32=False):
+    """Y (M, out) = X W^T for MXFP4 weights W (out, in) and 16-bit X (M, in).
+    Y is fp32 when y_f32, else X's dtype."""
+    M, n_in = X.shape
+    if codes.dim() != 2 or _mx4_cols(codes, scales) != n_in:
+        raise ValueError("codes must be (out, in / 2) for X (M, in)")
+    out, dev = codes.shape[0], X.device
+    ydt = torch.float32 if y_f32 else X.dtype
+    y = torch.empty((M, out), dtype=ydt, device=dev) if y is None else y
+    _need(y, "y", (M, out))
+    _launch("awq_mx4_gemm", dev, _dev(X, "X"), _dtype_code(X), M, n_in, _on(dev, codes, "codes", torch.uint8),
+            _on(dev, scales, "scales", torch.uint8), out, _on(dev, y, "y", ydt), _DTYPE[ydt])
+    return y
+
+
+def mx4_gemm_a4(x_codes, x_scales, codes, scales, dtype=torch.bfloat16, y=None):
+    """Y (M, out) = X W^T as `dtype`, X (M, in) and W (out, in) both MXFP4 (X as
+    mx4_quantize writes it)."""
+    n_in = _mx4_cols(x_codes, x_scales, "x_")
+    if x_codes.dim() != 2 or codes.dim() != 2 or _mx4_cols(codes, scales) != n_in:
+        raise ValueError("x_codes must be (M, in / 2) and codes (out, in / 2)")
+    M, out, dev = x_codes.shape[0], codes.shape[0], x_codes.device
+    y = torch.empty((M, out), dtype=dtype, device=dev) if y is None else y
+    _need(y, "y", (M, out))
+    _launch("awq_mx4_gemm_a4", dev, _dev(x_codes, "x_codes", torch.uint8), _on(dev, x_scales, "x_scales", torch.uint8),
+            M, n_in, _on(dev, codes, "codes", torch.uint8), _on(dev, scales, "scales", torch.uint8), out,
+            _on(dev, y, "y", dtype), _dtype_code(y))
+    return y
+
+
+def mx4_moe_workspace_size(M, inter, top_k):
+    return int(lib().awq_mx4_moe_workspace_size(M, inter, top_k))
+
+
+def mx4_moe(X, router, gate_up, gate_up_scales, down, down_scales, top_k, renorm=True, y=None, workspace=None):
+    """A mixture-of-experts layer on up to MX4_MOE_MAX_TOKENS tokens: routing by
+    softmax over X router^T (renorm: the chosen weights divided by their sum),
+    SwiGLU experts in MXFP4. X (M, hidden), router (experts, hidden) fp16 / bf16;
+    gate_up codes (experts, 2 inter, hidden / 2), the gate rows first; down codes
+    (experts, hidden, inter / 2); scales as mx4_quantize writes them."""
+    M, hidden = X.shape
+    experts = router.shape[0]
+    if gate_up.dim() != 3 or down.dim() != 3 or _mx4_cols(gate_up, gate_up_scales, "gate_up_") != hidden:
+        raise ValueError("gate_up must be (experts, 2 inter, hidden / 2)")
+    inter = _mx4_cols(down, down_scales, "down_")
+    _need(router, "router", (experts, hidden))
+    _need(gate_up, "gate_up", (experts, 2 * inter, hidden // 2))
+    _need(down, "down", (experts, hidden, inter // 2))
+    dev = X.device
+    y = torch.empty_like(X) if y is None else y
+    _need(y, "y", (M, hidden))
+    ws = _workspace(mx4_moe_workspace_size(M, inter, top_k), dev, workspace)
+    _launch("awq_mx4_moe", dev, _dev(X, "X"), _dtype_code(X), M, hidden, inter, experts, top_k, int(bool(renorm)),
+            _on(dev, router, "router", X.dtype), _on(dev, gate_up, "gate_up", torch.uint8),
+            _on(dev, gate_up_scales, "gate_up_scales", torch.uint8), _on(dev, down, "down", torch.uint8),
+            _on(dev, down_scales, "down_scales", torch.uint8), _on(dev, y, "y", X.dtype), _on(dev, ws, "workspace"),
+            ws.numel() * ws.element_size())
     return y
 
 

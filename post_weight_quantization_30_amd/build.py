@@ -16,7 +16,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libawq.so")
-SOURCES = ["abi.hip", "k_stats.hip", "k_search.hip", "k_pack.hip", "k_clip.hip", "k_fold.hip", "k_qgemm.hip", "k_gptq.hip"]
+SOURCES = ["abi.hip", "k_stats.hip", "k_search.hip", "k_pack.hip", "k_clip.hip", "k_fold.hip", "k_qgemm.hip", "k_gptq.hip",
+           "k_mx4.hip", "k_mx4_gemm.hip", "k_mx4_moe.hip"]
 # k_search16.hip is compiled once per (operand type, group size), in parallel:
 # (source, extra flags, object name).
 VARIANTS = [("k_search16.hip", [f"-DAWQ_S16_T={t}", f"-DAWQ_S16_G={g}"], f"k_search16_{t}_g{g}.o")

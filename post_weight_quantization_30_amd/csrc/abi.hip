@@ -452,4 +452,123 @@ int awq_quantize_pack_clip(const void *W, int dtype, int64_t out, int64_t in, co
                                        scales, zeros, (hipStream_t)stream));
 }
 
+namespace {
+
+// A matrix (rows, in) of MXFP4 blocks; the launches count chunks of 8 values
+// in blocks of 1024 chunks.
+int mx4_shape(int64_t rows, int64_t in)
+{
+    if (rows < 1 || in < 1 || in % AWQ_MX4_BLOCK != 0 || rows > INT64_MAX / in)
+        return AWQ_ERR_INVALID_ARG;
+    if (rows * in > (int64_t)1 << 43 || in > (int64_t)1 << 30)
+        return AWQ_ERR_UNSUPPORTED;
+    return AWQ_OK;
+}
+
+int mx4_gemm_shape(int64_t M, int64_t in, int64_t out)
+{
+    if (M < 1 || out < 1 || in < 1 || in % AWQ_MX4_BLOCK != 0 || out > INT64_MAX / in || M > INT64_MAX / in ||
+        M > INT64_MAX / out)
+        return AWQ_ERR_INVALID_ARG;
+    if (M > 65535LL * 32 || in > (int64_t)1 << 30 || (out + 15) / 16 > (int64_t)0x7fffffff)
+        return AWQ_ERR_UNSUPPORTED;
+    return AWQ_OK;
+}
+
+}  // namespace
+
+int awq_mx4_quantize(const void *W, int dtype, int64_t rows, int64_t in, const float *s, uint8_t *codes,
+                     uint8_t *scales, void *stream)
+{
+    if (!W || !codes || !scales || !valid_dtype(dtype))
+        return AWQ_ERR_INVALID_ARG;
+    int st = mx4_shape(rows, in);
+    if (st != AWQ_OK)
+        return st;
+    if (!aligned16(W) || !aligned16(s) || !aligned16(codes))
+        return AWQ_ERR_UNSUPPORTED;
+    return hip_status(awq::launch_mx4_quantize(W, dtype, rows, in, s, codes, scales, (hipStream_t)stream));
+}
+
+int awq_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t in, void *out, int dtype,
+                       void *stream)
+{
+    if (!codes || !scales || !out || !valid_dtype(dtype))
+        return AWQ_ERR_INVALID_ARG;
+    int st = mx4_shape(rows, in);
+    if (st != AWQ_OK)
+        return st;
+    if (!aligned16(codes) || !aligned16(out))
+        return AWQ_ERR_UNSUPPORTED;
+    return hip_status(awq::launch_mx4_dequantize(codes, scales, rows, in, out, dtype, (hipStream_t)stream));
+}
+
+int awq_mx4_gemm(const void *X, int x_dtype, int64_t M, int64_t in, const uint8_t *codes, const uint8_t *scales,
+                 int64_t out, void *Y, int y_dtype, void *stream)
+{
+    if (!X || !codes || !scales || !Y || !valid_dtype(x_dtype) || !valid_dtype(y_dtype) ||
+        (y_dtype != AWQ_F32 && y_dtype != x_dtype))
+        return AWQ_ERR_INVALID_ARG;
+    int st = mx4_gemm_shape(M, in, out);
+    if (st != AWQ_OK)
+        return st;
+    if (x_dtype == AWQ_F32 || !aligned16(X) || !aligned16(codes))
+        return AWQ_ERR_UNSUPPORTED;
+    return hip_status(awq::launch_mx4_gemm(X, x_dtype, M, in, codes, scales, out, Y, y_dtype == AWQ_F32,
+                                           (hipStream_t)stream));
+}
+
+int awq_mx4_gemm_a4(const uint8_t *xcodes, const uint8_t *xscales, int64_t M, int64_t in, const uint8_t *codes,
+                    const uint8_t *scales, int64_t out, void *Y, int y_dtype, void *stream)
+{
+    if (!xcodes || !xscales || !codes || !scales || !Y || !valid_dtype(y_dtype))
+        return AWQ_ERR_INVALID_ARG;
+    int st = mx4_gemm_shape(M, in, out);
+    if (st != AWQ_OK)
+        return st;
+    if (!aligned16(xcodes) || !aligned16(codes))
+        return AWQ_ERR_UNSUPPORTED;
+    return hip_status(awq::launch_mx4_gemm_a4(xcodes, xscales, M, in, codes, scales, out, Y, y_dtype,
+                                              (hipStream_t)stream));
+}
+
+namespace {
+
+int mx4_moe_shape(int64_t M, int64_t inter, int top_k)
+{
+    if (M < 1 || top_k < 1 || inter < 1 || inter % AWQ_MX4_BLOCK != 0)
+        return AWQ_ERR_INVALID_ARG;
+    if (M > AWQ_MX4_MOE_MAX_TOKENS || top_k > AWQ_MX4_MOE_MAX_TOPK || inter > (int64_t)1 << 20)
+        return AWQ_ERR_UNSUPPORTED;
+    return AWQ_OK;
+}
+
+}  // namespace
+
+size_t awq_mx4_moe_workspace_size(int64_t M, int64_t inter, int top_k)
+{
+    return mx4_moe_shape(M, inter, top_k) == AWQ_OK ? awq::mx4_moe_ws_layout(M, inter, top_k).total : 0;
+}
+
+int awq_mx4_moe(const void *X, int dtype, int64_t M, int64_t hidden, int64_t inter, int experts, int top_k, int renorm,
+                const void *router, const uint8_t *gu_codes, const uint8_t *gu_scales, const uint8_t *dn_codes,
+                const uint8_t *dn_scales, void *Y, void *ws, size_t ws_bytes, void *stream)
+{
+    if (!X || !router || !gu_codes || !gu_scales || !dn_codes || !dn_scales || !Y || !valid_dtype(dtype) ||
+        hidden < 1 || hidden % AWQ_MX4_BLOCK != 0 || experts < 1 || top_k > experts)
+        return AWQ_ERR_INVALID_ARG;
+    int st = mx4_moe_shape(M, inter, top_k);
+    if (st != AWQ_OK)
+        return st;
+    if (dtype == AWQ_F32 || experts > AWQ_MX4_MOE_MAX_EXPERTS || hidden > (int64_t)1 << 20 || !aligned16(X) ||
+        !aligned16(router) || !aligned16(gu_codes) || !aligned16(dn_codes))
+        return AWQ_ERR_UNSUPPORTED;
+    if (!ws || ws_bytes < awq::mx4_moe_ws_layout(M, inter, top_k).total)
+        return AWQ_ERR_WORKSPACE;
+    if (!aligned16(ws))
+        return AWQ_ERR_UNSUPPORTED;
+    return hip_status(awq::launch_mx4_moe(X, dtype, (int)M, (int)hidden, (int)inter, experts, top_k, renorm, router,
+                                          gu_codes, gu_scales, dn_codes, dn_scales, Y, ws, (hipStream_t)stream));
+}
+
 }  // extern "C"

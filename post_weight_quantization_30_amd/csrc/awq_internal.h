@@ -294,4 +294,33 @@ hipError_t launch_clip_search(const void *W, const void *X, int dtype, int64_t o
                               int64_t tokens, const float *s, int bits, int group, int mode,
                               int n_clip, float max_shrink, float *clip, double *sse, hipStream_t st);
 
+// MXFP4 (k_mx4.hip, k_mx4_gemm.hip, k_mx4_moe.hip).
+hipError_t launch_mx4_quantize(const void *W, int dtype, int64_t rows, int64_t in, const float *s, uint8_t *codes,
+                               uint8_t *scales, hipStream_t st);
+hipError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t in, void *out,
+                                 int dtype, hipStream_t st);
+hipError_t launch_mx4_gemm(const void *X, int dtype, int64_t M, int64_t in, const uint8_t *codes, const uint8_t *scales,
+                           int64_t out, void *Y, bool yf32, hipStream_t st);
+hipError_t launch_mx4_gemm_a4(const uint8_t *xcodes, const uint8_t *xscales, int64_t M, int64_t in,
+                              const uint8_t *codes, const uint8_t *scales, int64_t out, void *Y, int y_dtype,
+                              hipStream_t st);
+// Workspace of awq_mx4_moe: the routed experts and their weights, (M, top_k),
+// and p h of every pair, (M top_k, inter) in the activations' type.
+struct Mx4MoeWs {
+    size_t ids_off, w_off, h_off, total;
+};
+inline Mx4MoeWs mx4_moe_ws_layout(int64_t M, int64_t inter, int top_k)
+{
+    Mx4MoeWs w;
+    const size_t pairs = (size_t)(M * top_k);
+    w.ids_off = 0;
+    w.w_off = align256(pairs * sizeof(int32_t));
+    w.h_off = w.w_off + align256(pairs * sizeof(float));
+    w.total = w.h_off + align256(pairs * (size_t)inter * 2);
+    return w;
+}
+hipError_t launch_mx4_moe(const void *X, int dtype, int M, int hidden, int inter, int experts, int top_k, int renorm,
+                          const void *router, const uint8_t *gu_codes, const uint8_t *gu_scales,
+                          const uint8_t *dn_codes, const uint8_t *dn_scales, void *Y, void *ws, hipStream_t st);
+
 }  // namespace awq
