@@ -16,12 +16,13 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libawq.so")
-SOURCES = ["abi.hip", "k_stats.hip", "k_search.hip", "k_pack.hip", "k_clip.hip", "k_fold.hip", "k_qgemm.hip", "k_gptq.hip",
-           "k_mx4.hip", "k_mx4_gemm.hip", "k_mx4_moe.hip"]
+SOURCES = ["abi.hip", "k_stats.hip", "k_search.hip", "k_pack.hip", "k_clip.hip", "k_fold.hip", "k_qgemm.hip", "k_gptq.hip", "k_mx4.hip"]
 # k_search16.hip is compiled once per (operand type, group size), in parallel:
 # (source, extra flags, object name).
 VARIANTS = [("k_search16.hip", [f"-DAWQ_S16_T={t}", f"-DAWQ_S16_G={g}"], f"k_search16_{t}_g{g}.o")
             for t in ("f16", "bf16") for g in (32, 64, 128)]
+# C++20 for their template lambdas.
+VARIANTS += [(f, ["-std=c++20"], os.path.splitext(f)[0] + ".o") for f in ("k_mx4_gemm.hip", "k_mx4_moe.hip")]
 # Standalone measurement programs: the attainable MFMA peak (bench.py runs
 # it) and the microbenchmarks behind the kernel design (mb_gfx950).
 PROBES = [("mfma_peak.hip", os.path.join(PKG, "mfma_peak")),

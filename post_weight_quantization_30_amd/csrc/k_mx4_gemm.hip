@@ -59,32 +59,7 @@ __global__ __launch_bounds__(64 * W) void k_mx4_gemm_split(const void *__restric
     }
 
     f32x4 acc[MT][NT];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-            acc[mt][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-    Mx4Item<TX, MT, NT, U> a, b;
-    int i = wave * (4 * U);
-    const int step = W * (4 * U);
-    if (i < nb) {
-        mx4_load(a, rows, i, nb, c);
-        while (true) {
-            if (i + step < nb)
-                mx4_load(b, rows, i + step, nb, c);
-            mx4_compute(a, acc, i, nb, c);
-            i += step;
-            if (i >= nb)
-                break;
-            if (i + step < nb)
-                mx4_load(a, rows, i + step, nb, c);
-            mx4_compute(b, acc, i, nb, c);
-            i += step;
-            if (i >= nb)
-                break;
-        }
-    }
+    mx4_wave<TX, MT, NT, U>(rows, acc, wave * (4 * U), W * (4 * U), nb, c);
 
 #pragma unroll
     for (int t0 = 0; t0 < TILES; t0 += TG) {
@@ -114,16 +89,394 @@ hipError_t split(const void *X, const uint8_t *xs, int64_t M, int nb, const uint
     return hipGetLastError();
 }
 
+// ---------------------------------------------------------------------------
+// Many tokens: 32x32 matrix tiles.
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+__device__ __forceinline__ f32x16 mfma32(const bf16x8 &a, const bf16x8 &b, const f32x16 &c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mfma32(const f16x8 &a, const f16x8 &b, const f32x16 &c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+// Both operands MXFP4, 64 columns; byte S of the scale registers.
+template <int S>
+__device__ __forceinline__ f32x16 mfma32(const u32x4 &a, uint32_t sa, const u32x4 &b, uint32_t sb, const f32x16 &c)
+{
+    const i32x8 a8 = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+    const i32x8 b8 = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a8, b8, c, 4, 4, S, (int)sa, S, (int)sb);
+}
+
+// Tile of this block: the blocks of one XCD (every eighth) walk a contiguous
+// range of tiles, 16 token tiles by one row tile at a time, so that what they
+// read together stays in that XCD's L2.
+__device__ __forceinline__ bool tile_of_block(int64_t tm, int64_t tn, int64_t &m, int64_t &n)
+{
+    const int64_t tiles = tm * tn, chunk = (tiles + 7) / 8;
+    const int64_t t = (blockIdx.x & 7) * chunk + (blockIdx.x >> 3);
+    if ((blockIdx.x >> 3) >= chunk || t >= tiles)
+        return false;
+    const int64_t band = t / (16 * tn), first = band * 16, in_band = t - band * 16 * tn;
+    const int64_t h = tm - first < 16 ? tm - first : 16;
+    m = first + in_band % h;
+    n = in_band / h;
+    return true;
+}
+
+// The results of a wave's MT x NT tiles, tile (a, b) at token m0 + 32 a, row
+// n0 + 32 b: register i of lane (r, h) is token 8 (i / 4) + 4 h + i % 4, row r.
+template <typename TY, int MT, int NT>
+__device__ __forceinline__ void store_tiles(TY *__restrict__ Y, const f32x16 (&acc)[MT][NT], int64_t m0, int64_t n0,
+                                            int64_t M, int64_t out, int r, int h)
+{
+#pragma unroll
+    for (int a = 0; a < MT; ++a)
+#pragma unroll
+        for (int b = 0; b < NT; ++b) {
+            const int64_t n = n0 + 32 * b + r;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int64_t m = m0 + 32 * a + 8 * (i / 4) + 4 * h + i % 4;
+                if (m < M && n < out)
+                    Y[m * out + n] = static_cast<TY>(acc[a][b][i]);
+            }
+        }
+}
+
+// Columns up to which the tile kernels' 32-bit offsets within a tile hold.
+constexpr int64_t kTileMaxIn = (int64_t)1 << 21;
+
+// 16-bit activations. Block: 128 tokens x 256 rows, 4 waves of 128 x 64. A
+// step is 64 columns: 128 bytes of every activation row go to LDS as eight
+// 16-byte chunks, chunk q of row m at position q ^ (m & 7), so that the eight
+// rows which one 128-byte LDS cycle serves lie on distinct banks. Weights go
+// from memory straight to the registers of the wave that multiplies them: no
+// other wave has its rows, and one conversion there serves all 128 tokens.
+// Step k + 1 is fetched while step k is multiplied; two LDS buffers, one
+// barrier a step.
+// Lane (r, h) = (lane % 32, lane / 32) of a 32-row tile holds in k-step s of 4
+// columns 32 h + 8 s ... of the step: chunk 4 h + s of an activation row, word
+// s of block h of a weight row.
+template <typename TX, typename TY>
+__global__ __launch_bounds__(256, 2) void k_mx4_gemm_tile(const TX *__restrict__ X, int64_t M, int nb,
+                                                          const uint8_t *__restrict__ codes,
+                                                          const uint8_t *__restrict__ scales, int64_t out,
+                                                          TY *__restrict__ Y)
+{
+    typedef typename Vec8<TX>::type vec;
+    constexpr int MT = 4, NT = 2, BM = 128, BN = 256;
+    constexpr int CH = BM * 8 / 256;                   // activation chunks a thread moves in a step
+    __shared__ __align__(16) u32x4 lds[2][BM * 8];
+
+    int64_t m0, n0;
+    if (!tile_of_block((M + BM - 1) / BM, (out + BN - 1) / BN, m0, n0))
+        return;
+    m0 *= BM;
+    n0 *= BN;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 31, h = lane >> 5;
+    const int xrow = nb * 64;                          // bytes of an activation row
+    const int steps = (nb + 1) / 2, full = nb / 2;
+
+    // Addresses are a scalar base (this tile, this step) and a 32-bit offset a
+    // lane. Rows past the ends load the last row: their results are not stored.
+    const uint8_t *const xbase = (const uint8_t *)X + m0 * xrow;
+    const uint8_t *const wbase = codes + n0 * nb * 16, *const wsbase = scales + n0 * nb;
+    const uint32_t mlast = (uint32_t)(M - 1 - m0 < BM - 1 ? M - 1 - m0 : BM - 1);
+    const uint32_t nlast = (uint32_t)(out - 1 - n0 < BN - 1 ? out - 1 - n0 : BN - 1);
+    uint32_t xo[CH], wo[NT], wso[NT];
+    int xdst[CH];
+    const int xq = threadIdx.x & 7;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        const uint32_t row = (threadIdx.x + i * 256) >> 3;
+        xdst[i] = row * 8 + (xq ^ (row & 7));
+        xo[i] = (row < mlast ? row : mlast) * (uint32_t)xrow + xq * 16;
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        uint32_t n = 64 * wave + 32 * t + r;
+        n = n < nlast ? n : nlast;
+        wo[t] = n * (uint32_t)nb * 16 + h * 16;
+        wso[t] = n * (uint32_t)nb + h;
+    }
+
+    f32x16 acc[MT][NT];
+    u32x4 xr[CH], w[NT], wnext[NT];
+    uint32_t ws[NT], wsnext[NT];
+    bool bad = false;
+
+    // An odd last block: the step's second half loads the row's last block
+    // instead; zeros (under scale 1) take its place on the way to use.
+    auto fetch = [&](int k) {
+        const bool end = k >= full;
+        const uint32_t xback = end && xq >= 4 ? 64 : 0, wback = end && h ? 1 : 0;
+        const uint8_t *const px = xbase + (int64_t)k * 128, *const pw = wbase + (int64_t)k * 32;
+        const uint8_t *const ps = wsbase + k * 2;
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+            xr[i] = *reinterpret_cast<const u32x4 *>(px + (xo[i] - xback));
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            wnext[t] = *reinterpret_cast<const u32x4 *>(pw + (wo[t] - 16 * wback));
+            wsnext[t] = ps[wso[t] - wback];
+        }
+    };
+    auto stash = [&](int k) {
+        if (k >= full && xq >= 4)
+#pragma unroll
+            for (int i = 0; i < CH; ++i)
+                xr[i] = u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+            lds[k & 1][xdst[i]] = xr[i];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            w[t] = wnext[t];
+            ws[t] = k >= full && h ? 127 : wsnext[t];
+        }
+    };
+    auto xfrag = [&](int k, int t, int s) -> u32x4 {
+        const int row = 32 * t + r;
+        return lds[k & 1][row * 8 + ((4 * h + s) ^ (row & 7))];
+    };
+    auto contract = [&]<bool WIDE>() {
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+#pragma unroll
+            for (int b = 0; b < NT; ++b)
+                acc[a][b] = f32x16{};
+        fetch(0);
+        stash(0);
+        __syncthreads();
+        for (int k = 0; k < steps; ++k) {
+            if (k + 1 < steps)
+                fetch(k + 1);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                if constexpr (!WIDE) {
+                    vec wv[NT];
+#pragma unroll
+                    for (int b = 0; b < NT; ++b) {
+                        if constexpr (std::is_same<TX, f16>::value) {
+                            wv[b] = mx4_to_f16(w[b][s], mx4_scale(ws[b]));
+                            bad = bad || !mx4_fits_f16(ws[b]);
+                        } else {
+                            wv[b] = mx4_to_bf16(w[b][s], mx4_scale(ws[b]));
+                        }
+                    }
+#pragma unroll
+                    for (int a = 0; a < MT; ++a) {
+                        const vec x = __builtin_bit_cast(vec, xfrag(k, a, s));
+#pragma unroll
+                        for (int b = 0; b < NT; ++b)
+                            acc[a][b] = mfma32(x, wv[b], acc[a][b]);
+                    }
+                } else {
+                    __builtin_amdgcn_sched_barrier(0);
+                    bf16x8 wv[NT];
+#pragma unroll
+                    for (int b = 0; b < NT; ++b)
+                        wv[b] = mx4_to_bf16(w[b][s], mx4_scale(ws[b]));
+#pragma unroll
+                    for (int a = 0; a < MT; ++a) {
+                        bf16x8 hi, lo;
+                        split_f16(__builtin_bit_cast(f16x8, xfrag(k, a, s)), hi, lo);
+#pragma unroll
+                        for (int b = 0; b < NT; ++b) {
+                            acc[a][b] = mfma32(hi, wv[b], acc[a][b]);
+                            acc[a][b] = mfma32(lo, wv[b], acc[a][b]);
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+            }
+            if (k + 1 < steps)
+                stash(k + 1);
+            __syncthreads();
+        }
+    };
+    contract.template operator()<false>();
+    // fp16 activations under scales that fp16 cannot hold: all of it once more
+    // in the wide form (weights in bf16, activations as two bf16 parts)
+    if constexpr (std::is_same<TX, f16>::value)
+        if (__syncthreads_or(bad))
+            contract.template operator()<true>();
+    store_tiles<TY, MT, NT>(Y, acc, m0, n0 + 64 * wave, M, out, r, h);
+}
+
+// MXFP4 activations. Block: 256 x 256, 4 waves of 128 x 128 (256 accumulator
+// registers each, one wave a SIMD). Both operands through LDS: a step is 128
+// columns, per row four 16-byte blocks and four scale bytes. Block q of row m
+// lies at position q ^ (m / 2 & 3) of the row's 64 bytes: eight rows at a time
+// fall on distinct banks. Three buffers: while step k is multiplied, k + 1 is
+// complete and k + 2 is on its way, so one barrier a step suffices and the
+// first operands of the next step can be read before it.
+// Lane (r, h) holds in k-step s of 2 block 2 s + h of its row.
+template <typename TY>
+__global__ __launch_bounds__(256, 1) void k_mx4_gemm_tile4(const uint8_t *__restrict__ xcodes,
+                                                           const uint8_t *__restrict__ xscales, int64_t M, int nb,
+                                                           const uint8_t *__restrict__ codes,
+                                                           const uint8_t *__restrict__ scales, int64_t out,
+                                                           TY *__restrict__ Y)
+{
+    constexpr int MT = 4, NT = 4, B = 256, ST = 3;
+    __shared__ __align__(16) u32x4 lx[ST][B * 4], lw[ST][B * 4];
+    __shared__ uint32_t lxs[ST][B], lws[ST][B];
+
+    int64_t m0, n0;
+    if (!tile_of_block((M + B - 1) / B, (out + B - 1) / B, m0, n0))
+        return;
+    m0 *= B;
+    n0 *= B;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 31, h = lane >> 5, wm = wave >> 1, wn = wave & 1;
+    const int steps = (nb + 3) / 4, full = nb / 4;
+
+    const uint8_t *const xbase = xcodes + m0 * nb * 16, *const xsbase = xscales + m0 * nb;
+    const uint8_t *const wbase = codes + n0 * nb * 16, *const wsbase = scales + n0 * nb;
+    const uint32_t mlast = (uint32_t)(M - 1 - m0 < B - 1 ? M - 1 - m0 : B - 1);
+    const uint32_t nlast = (uint32_t)(out - 1 - n0 < B - 1 ? out - 1 - n0 : B - 1);
+    const int q = threadIdx.x & 3;
+    uint32_t xo[4], wo[4];
+    int dst[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t row = (threadIdx.x + i * 256) >> 2;
+        dst[i] = row * 4 + (q ^ (row >> 1 & 3));
+        xo[i] = (row < mlast ? row : mlast) * (uint32_t)nb * 16 + q * 16;
+        wo[i] = (row < nlast ? row : nlast) * (uint32_t)nb * 16 + q * 16;
+    }
+    const uint32_t srow = threadIdx.x;                 // the row whose scales this thread moves
+    const uint32_t xso = (srow < mlast ? srow : mlast) * (uint32_t)nb, wso = (srow < nlast ? srow : nlast) * (uint32_t)nb;
+
+    u32x4 xr[4], wr[4];
+    uint32_t xsr, wsr;
+    // The last step of a row that ends inside it: zeros under scale 1 past the end.
+    auto fetch = [&](int k) {
+        const uint8_t *const px = xbase + (int64_t)k * 64, *const pw = wbase + (int64_t)k * 64;
+        const uint8_t *const pxs = xsbase + k * 4, *const pws = wsbase + k * 4;
+        if (k < full) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                xr[i] = *reinterpret_cast<const u32x4 *>(px + xo[i]);
+                wr[i] = *reinterpret_cast<const u32x4 *>(pw + wo[i]);
+            }
+            __builtin_memcpy(&xsr, pxs + xso, 4);
+            __builtin_memcpy(&wsr, pws + wso, 4);
+        } else {
+            const int valid = nb - 4 * k;              // 1 .. 3 blocks
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                xr[i] = wr[i] = u32x4{0, 0, 0, 0};
+                if (q < valid) {
+                    xr[i] = *reinterpret_cast<const u32x4 *>(px + xo[i]);
+                    wr[i] = *reinterpret_cast<const u32x4 *>(pw + wo[i]);
+                }
+            }
+            xsr = wsr = 0x7F7F7F7Fu;
+            for (int i = 0; i < valid; ++i) {
+                xsr = (xsr & ~(0xFFu << (8 * i))) | (uint32_t)pxs[xso + i] << (8 * i);
+                wsr = (wsr & ~(0xFFu << (8 * i))) | (uint32_t)pws[wso + i] << (8 * i);
+            }
+        }
+    };
+    auto stash = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            lx[buf][dst[i]] = xr[i];
+            lw[buf][dst[i]] = wr[i];
+        }
+        lxs[buf][srow] = xsr;
+        lws[buf][srow] = wsr;
+    };
+
+    f32x16 acc[MT][NT];
+#pragma unroll
+    for (int a = 0; a < MT; ++a)
+#pragma unroll
+        for (int b = 0; b < NT; ++b)
+            acc[a][b] = f32x16{};
+    // this lane's rows: 128 wm + 32 a + r and 128 wn + 32 b + r; the swizzle
+    // depends on r alone
+    const int xr0 = (128 * wm + r) * 4, wr0 = (128 * wn + r) * 4, swz = r >> 1 & 3;
+
+    fetch(0);
+    stash(0);
+    if (steps > 1)
+        fetch(1);
+    __syncthreads();
+    int cur = 0, nxt = 1;
+    for (int k = 0; k < steps; ++k) {
+        // step k + 1 (in registers) goes to its buffer, step k + 2 on its way
+        if (k + 1 < steps)
+            stash(nxt);
+        if (k + 2 < steps)
+            fetch(k + 2);
+        uint32_t sa[MT], sb[NT];
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+            sa[a] = lxs[cur][128 * wm + 32 * a + r] >> (8 * h);
+#pragma unroll
+        for (int b = 0; b < NT; ++b)
+            sb[b] = lws[cur][128 * wn + 32 * b + r] >> (8 * h);
+        u32x4 x[2][MT], w[2][NT];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int p = (2 * s + h) ^ swz;
+#pragma unroll
+            for (int a = 0; a < MT; ++a)
+                x[s][a] = lx[cur][xr0 + 128 * a + p];
+#pragma unroll
+            for (int b = 0; b < NT; ++b)
+                w[s][b] = lw[cur][wr0 + 128 * b + p];
+        }
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+#pragma unroll
+            for (int b = 0; b < NT; ++b)
+                acc[a][b] = mfma32<0>(x[0][a], sa[a], w[0][b], sb[b], acc[a][b]);
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+#pragma unroll
+            for (int b = 0; b < NT; ++b)
+                acc[a][b] = mfma32<2>(x[1][a], sa[a], w[1][b], sb[b], acc[a][b]);
+        __syncthreads();
+        cur = nxt;
+        nxt = nxt == ST - 1 ? 0 : nxt + 1;
+    }
+    store_tiles<TY, MT, NT>(Y, acc, m0 + 128 * wm, n0 + 128 * wn, M, out, r, h);
+}
+
+inline int64_t tiles_of(int64_t n, int64_t size) { return (n + size - 1) / size; }
+// Whole multiples of 8: see tile_of_block.
+inline uint32_t tile_grid(int64_t tiles) { return (uint32_t)((tiles + 7) / 8 * 8); }
+
 template <typename TX, typename TY>
 hipError_t gemm(const void *X, const uint8_t *xs, int64_t M, int nb, const uint8_t *codes, const uint8_t *scales,
                 int64_t out, void *Y, hipStream_t st)
 {
     if (M <= 16)
         return split<TX, TY, 1, 1, 4>(X, xs, M, nb, codes, scales, out, Y, st);
-    if constexpr (std::is_same<TX, Mx4Act>::value)
+    if constexpr (std::is_same<TX, Mx4Act>::value) {
+        if (nb * 32 <= kTileMaxIn && tiles_of(M, 256) * tiles_of(out, 256) >= 64) {
+            k_mx4_gemm_tile4<TY><<<tile_grid(tiles_of(M, 256) * tiles_of(out, 256)), 256, 0, st>>>(
+                (const uint8_t *)X, xs, M, nb, codes, scales, out, (TY *)Y);
+            return hipGetLastError();
+        }
         return split<TX, TY, 4, 4, 1>(X, xs, M, nb, codes, scales, out, Y, st);
-    else
+    } else {
+        if (nb * 32 <= kTileMaxIn && tiles_of(M, 128) * tiles_of(out, 256) >= 128) {
+            k_mx4_gemm_tile<TX, TY><<<tile_grid(tiles_of(M, 128) * tiles_of(out, 256)), 256, 0, st>>>(
+                (const TX *)X, M, nb, codes, scales, out, (TY *)Y);
+            return hipGetLastError();
+        }
         return split<TX, TY, 4, 2, 1>(X, xs, M, nb, codes, scales, out, Y, st);
+    }
 }
 
 }  // namespace

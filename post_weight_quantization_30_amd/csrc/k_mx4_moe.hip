@@ -169,29 +169,7 @@ __device__ __forceinline__ void up_tokens(const TX *__restrict__ X, int nb, cons
         rows.xs[mt] = nullptr;
     }
     f32x4 acc[MT][2];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-        acc[mt][0] = acc[mt][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-    Mx4Item<TX, MT, 2, U> a, b;
-    int i = wave * (4 * U);
-    const int step = kUpWaves * (4 * U);
-    if (i < nb) {
-        mx4_load(a, rows, i, nb, c);
-        while (true) {
-            if (i + step < nb)
-                mx4_load(b, rows, i + step, nb, c);
-            mx4_compute(a, acc, i, nb, c);
-            i += step;
-            if (i >= nb)
-                break;
-            if (i + step < nb)
-                mx4_load(a, rows, i + step, nb, c);
-            mx4_compute(b, acc, i, nb, c);
-            i += step;
-            if (i >= nb)
-                break;
-        }
-    }
+    mx4_wave<TX, MT, 2, U>(rows, acc, wave * (4 * U), kUpWaves * (4 * U), nb, c);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
         __syncthreads();           // the previous tile's sums are read
@@ -311,9 +289,8 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_mx4_moe_down(const TX *__re
     const int nb = inter / kMxBlock, per = (nb + 4 * U - 1) / (4 * U), items = active * per;
     const int n = blockIdx.x * 16 + r;
     f32x4 acc[MT][1];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-        acc[mt][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+    bool bad = false;
+    mx4_zero(acc);
 
     auto load = [&](Mx4Item<TX, MT, 1, U> &it, int i) {
         const int a = i / per, b0 = (i - a * per) * 4 * U;
@@ -329,13 +306,11 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_mx4_moe_down(const TX *__re
         }
         mx4_load(it, rows, b0, nb, c);
     };
-    auto compute = [&](Mx4Item<TX, MT, 1, U> &it, int i) {
+    auto compute = [&]<bool WIDE>(Mx4Item<TX, MT, 1, U> &it, int i) {
         const int a = i / per, b0 = (i - a * per) * 4 * U;
         f32x4 part[MT][1];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-            part[mt][0] = f32x4{0.f, 0.f, 0.f, 0.f};
-        mx4_compute(it, part, b0, nb, c);
+        mx4_zero(part);
+        mx4_compute<WIDE>(it, part, b0, nb, c, bad);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -350,16 +325,26 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_mx4_moe_down(const TX *__re
         while (true) {
             if (i + kDownWaves < items)
                 load(B, i + kDownWaves);
-            compute(A, i);
+            compute.template operator()<false>(A, i);
             i += kDownWaves;
             if (i >= items)
                 break;
             if (i + kDownWaves < items)
                 load(A, i + kDownWaves);
-            compute(B, i);
+            compute.template operator()<false>(B, i);
             i += kDownWaves;
             if (i >= items)
                 break;
+        }
+        if constexpr (std::is_same<TX, f16>::value) {
+            if (__any(bad)) {          // scales that fp16 cannot hold: once more in the wide form
+                mx4_zero(acc);
+#pragma unroll 1
+                for (i = wave; i < items; i += kDownWaves) {
+                    load(A, i);
+                    compute.template operator()<true>(A, i);
+                }
+            }
         }
     }
 #pragma unroll

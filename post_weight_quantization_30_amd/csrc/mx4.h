@@ -139,9 +139,12 @@ __device__ __forceinline__ void mx4_load(Mx4Item<TX, MT, NT, U> &it, const Mx4Ro
 }
 
 // acc += the item's products. A lane whose block lies past the row's end
-// multiplies zeros (its weights are then finite: scale 1).
-template <typename TX, int MT, int NT, int U>
-__device__ __forceinline__ void mx4_compute(Mx4Item<TX, MT, NT, U> &it, f32x4 (&acc)[MT][NT], int b0, int nb, int c)
+// multiplies zeros (its weights are then finite: scale 1). WIDE is for fp16
+// activations under scales that fp16 cannot hold: weights in bf16, activations
+// as two bf16 parts. The plain form reports such scales in `bad`.
+template <bool WIDE, typename TX, int MT, int NT, int U>
+__device__ __forceinline__ void mx4_compute(Mx4Item<TX, MT, NT, U> &it, f32x4 (&acc)[MT][NT], int b0, int nb, int c,
+                                            bool &bad)
 {
     if (b0 + 4 * U > nb) {
 #pragma unroll
@@ -172,52 +175,93 @@ __device__ __forceinline__ void mx4_compute(Mx4Item<TX, MT, NT, U> &it, f32x4 (&
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
                     acc[mt][nt] = mx4_mfma(it.x[mt][u].q, it.x[mt][u].s, it.w[nt][u], it.ws[nt][u], acc[mt][nt]);
+    } else if constexpr (!WIDE) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float s = mx4_scale(it.ws[nt][u]);
+                if constexpr (std::is_same<TX, f16>::value)
+                    bad = bad || !mx4_fits_f16(it.ws[nt][u]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    typename Vec8<TX>::type w;
+                    if constexpr (std::is_same<TX, f16>::value)
+                        w = mx4_to_f16(it.w[nt][u][k], s);
+                    else
+                        w = mx4_to_bf16(it.w[nt][u][k], s);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+                        acc[mt][nt] = mx4_mfma(it.x[mt][u].v[k], w, acc[mt][nt]);
+                }
+            }
     } else {
-        bool f16_ok = true;
-        if constexpr (std::is_same<TX, f16>::value) {
-            bool fits = true;
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    fits = fits && mx4_fits_f16(it.ws[nt][u]);
-            f16_ok = __all(fits);
-        }
-        if (f16_ok) {
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+                for (int k = 0; k < 4; ++k) {
+                    __builtin_amdgcn_sched_barrier(0);       // one split at a time: registers
+                    bf16x8 hi, lo;
+                    split_f16(it.x[mt][u].v[k], hi, lo);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const float s = mx4_scale(it.ws[nt][u]);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        typename Vec8<TX>::type w;
-                        if constexpr (std::is_same<TX, f16>::value)
-                            w = mx4_to_f16(it.w[nt][u][k], s);
-                        else
-                            w = mx4_to_bf16(it.w[nt][u][k], s);
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt)
-                            acc[mt][nt] = mx4_mfma(it.x[mt][u].v[k], w, acc[mt][nt]);
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const bf16x8 w = mx4_to_bf16(it.w[nt][u][k], mx4_scale(it.ws[nt][u]));
+                        acc[mt][nt] = mx4_mfma(hi, w, acc[mt][nt]);
+                        acc[mt][nt] = mx4_mfma(lo, w, acc[mt][nt]);
                     }
                 }
-        } else if constexpr (std::is_same<TX, f16>::value) {
-            // scales outside fp16's range: weights in bf16, activations as two bf16 parts
+    }
+}
+
+template <int MT, int NT> __device__ __forceinline__ void mx4_zero(f32x4 (&acc)[MT][NT])
+{
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        bf16x8 hi, lo;
-                        split_f16(it.x[mt][u].v[k], hi, lo);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            const bf16x8 w = mx4_to_bf16(it.w[nt][u][k], mx4_scale(it.ws[nt][u]));
-                            acc[mt][nt] = mx4_mfma(hi, w, acc[mt][nt]);
-                            acc[mt][nt] = mx4_mfma(lo, w, acc[mt][nt]);
-                        }
-                    }
+        for (int nt = 0; nt < NT; ++nt)
+            acc[mt][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+}
+
+// One wave's share of a contraction: the items that begin at blocks first,
+// first + step, ... of the rows, each in flight while the one before it is
+// multiplied. fp16 activations: where a scale turns out not to fit, all of it
+// once more in the wide form (real weights never need it, so the hot loop
+// carries no branch and no registers for it).
+template <typename TX, int MT, int NT, int U>
+__device__ __forceinline__ void mx4_wave(const Mx4Rows<TX, MT, NT> &rows, f32x4 (&acc)[MT][NT], int first, int step,
+                                         int nb, int c)
+{
+    mx4_zero(acc);
+    if (first >= nb)
+        return;
+    Mx4Item<TX, MT, NT, U> a, b;
+    bool bad = false;
+    int i = first;
+    mx4_load(a, rows, i, nb, c);
+    while (true) {
+        if (i + step < nb)
+            mx4_load(b, rows, i + step, nb, c);
+        mx4_compute<false>(a, acc, i, nb, c, bad);
+        i += step;
+        if (i >= nb)
+            break;
+        if (i + step < nb)
+            mx4_load(a, rows, i + step, nb, c);
+        mx4_compute<false>(b, acc, i, nb, c, bad);
+        i += step;
+        if (i >= nb)
+            break;
+    }
+    if constexpr (std::is_same<TX, f16>::value) {
+        if (__any(bad)) {
+            mx4_zero(acc);
+#pragma unroll 1
+            for (i = first; i < nb; i += step) {
+                mx4_load(a, rows, i, nb, c);
+                mx4_compute<true>(a, acc, i, nb, c, bad);
+            }
         }
     }
 }
