@@ -348,8 +348,8 @@ size_t awq_gptq_workspace_size(int64_t out, int64_t in);
  *      several layers' or experts' stacked, or activations.
  * awq_mx4_dequantize: out (rows, in) of `dtype` = the values, rounded to nearest
  * even where `dtype` does not hold them (bf16 and fp32 hold all below 2^128).
- * AWQ_ERR_UNSUPPORTED: W, s, codes or out not 16-byte aligned, or a matrix of
- * more than 2^43 values. */
+ * AWQ_ERR_UNSUPPORTED: W, s, codes or out not 16-byte aligned, a matrix of more
+ * than 2^43 values, or `in` above 2^28. */
 #define AWQ_MX4_BLOCK 32
 int awq_mx4_quantize(const void *W, int dtype, int64_t rows, int64_t in, const float *s, uint8_t *codes,
                      uint8_t *scales, void *stream);
@@ -367,7 +367,7 @@ int awq_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows
  * rounding to a 16-bit Y. A row of X or W that holds a NaN makes its own
  * outputs NaN and no others.
  * AWQ_ERR_UNSUPPORTED: x_dtype AWQ_F32, X or codes (xcodes) not 16-byte aligned,
- * M above 2 097 120, or `in` above 2^30. */
+ * M above 2 097 120, or `in` above 2^28. */
 int awq_mx4_gemm(const void *X, int x_dtype, int64_t M, int64_t in, const uint8_t *codes,
                  const uint8_t *scales, int64_t out, void *Y, int y_dtype, void *stream);
 int awq_mx4_gemm_a4(const uint8_t *xcodes, const uint8_t *xscales, int64_t M, int64_t in,
@@ -388,7 +388,7 @@ int awq_mx4_gemm_a4(const uint8_t *xcodes, const uint8_t *xscales, int64_t M, in
  *           expert the inter gate rows, then the inter up rows.
  *   dn_codes, dn_scales: device, the MXFP4 matrix (experts * hidden, inter).
  *   Y:      device (M, hidden) of `dtype` (output); must not overlap an input.
- *   ws:     device scratch of awq_mx4_moe_workspace_size(M, inter, top_k) bytes
+ *   ws:     device scratch of awq_mx4_moe_workspace_size(M, hidden, inter, top_k) bytes
  *           (0 for sizes that the call refuses). Calls that overlap in time need
  *           a workspace each.
  * hidden and inter must be multiples of 32, 1 <= top_k <= experts.
@@ -403,7 +403,7 @@ int awq_mx4_moe(const void *X, int dtype, int64_t M, int64_t hidden, int64_t int
                 int renorm, const void *router, const uint8_t *gu_codes, const uint8_t *gu_scales,
                 const uint8_t *dn_codes, const uint8_t *dn_scales, void *Y, void *ws, size_t ws_bytes,
                 void *stream);
-size_t awq_mx4_moe_workspace_size(int64_t M, int64_t inter, int top_k);
+size_t awq_mx4_moe_workspace_size(int64_t M, int64_t hidden, int64_t inter, int top_k);
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char *awq_status_string(int status);

@@ -5,6 +5,7 @@ the caller's current torch stream. There is no CPU fallback: if the library
 is not built, or a tensor is not on the GPU, these functions raise.
 """
 import ctypes
+import math
 import os
 
 import torch
@@ -103,7 +104,7 @@ def lib():
         L.awq_mx4_gemm_a4.restype = cint
         L.awq_mx4_moe.argtypes = [vp, cint, i64, i64, i64, cint, cint, cint, vp, u8, u8, u8, u8, vp, vp, sz, vp]
         L.awq_mx4_moe.restype = cint
-        L.awq_mx4_moe_workspace_size.argtypes = [i64, i64, cint]
+        L.awq_mx4_moe_workspace_size.argtypes = [i64, i64, i64, cint]
         L.awq_mx4_moe_workspace_size.restype = sz
         L.awq_status_string.argtypes = [cint]
         L.awq_status_string.restype = ctypes.c_char_p
@@ -381,17 +382,26 @@ MX4_MOE_MAX_TOKENS, MX4_MOE_MAX_TOPK, MX4_MOE_MAX_EXPERTS = 64, 16, 256
 
 def _launch(name, device, *args):
     """Calls the library on `device` and the stream that is current there."""
-    if device.index == torch.cuda.current_device():
-        _check(name, getattr(lib(), name)(*args, _stream()))
+    fn, index = getattr(lib(), name), device.index
+    if index == torch.cuda.current_device():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(device):
-            _check(name, getattr(lib(), name)(*args, _stream()))
+        with torch.cuda.device(index):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    _check(name, status)
 
 
-def _on(device, t, name, dtype=None):
-    if t.device != device:
+def _ptr(t, name, device=None, dtype=None):
+    """Address of a contiguous GPU tensor (on `device`, of `dtype`)."""
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a GPU tensor")
+    if device is not None and t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
-    return _dev(t, name, dtype)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    return t.data_ptr()
 
 
 def _mx4_cols(codes, scales, what=""):
@@ -405,33 +415,28 @@ def _mx4_cols(codes, scales, what=""):
 def mx4_quantize(W, s=None, codes=None, scales=None):
     """W (..., in) to MXFP4 along its last dimension: (codes uint8 (..., in / 2),
     scales uint8 (..., in / 32)); with `s` (fp32 [in]) of W diag(s)."""
-    if W.dim() < 2 or W.shape[-1] % MX4_BLOCK != 0:
+    shape = W.shape
+    if len(shape) < 2 or shape[-1] % MX4_BLOCK != 0:
         raise ValueError(f"W must be (..., in) with in a multiple of {MX4_BLOCK}")
-    n_in = W.shape[-1]
-    if codes is None:
-        codes = torch.empty(W.shape[:-1] + (n_in // 2,), dtype=torch.uint8, device=W.device)
-    if scales is None:
-        scales = torch.empty(W.shape[:-1] + (n_in // MX4_BLOCK,), dtype=torch.uint8, device=W.device)
-    _need(codes, "codes", W.shape[:-1] + (n_in // 2,))
-    _need(scales, "scales", W.shape[:-1] + (n_in // MX4_BLOCK,))
+    n_in, dev, rows = shape[-1], W.device, shape[0] if len(shape) == 2 else math.prod(shape[:-1])
+    cshape, sshape = (*shape[:-1], n_in // 2), (*shape[:-1], n_in // MX4_BLOCK)
+    codes = torch.empty(cshape, dtype=torch.uint8, device=dev) if codes is None else _need(codes, "codes", cshape)
+    scales = torch.empty(sshape, dtype=torch.uint8, device=dev) if scales is None else _need(scales, "scales", sshape)
     if s is not None:
-        _need(s, "s", (n_in,))
-    dev = W.device
-    _launch("awq_mx4_quantize", dev, _dev(W, "W"), _dtype_code(W), W.numel() // max(n_in, 1), n_in,
-            None if s is None else _on(dev, s, "s", torch.float32), _on(dev, codes, "codes", torch.uint8),
-            _on(dev, scales, "scales", torch.uint8))
+        s = _ptr(_need(s, "s", (n_in,)), "s", dev, torch.float32)
+    _launch("awq_mx4_quantize", dev, _ptr(W, "W"), _dtype_code(W), rows, n_in, s,
+            _ptr(codes, "codes", dev, torch.uint8), _ptr(scales, "scales", dev, torch.uint8))
     return codes, scales
 
 
 def mx4_dequantize(codes, scales, dtype=torch.bfloat16, out=None):
     """The values (..., in) that MXFP4 codes and scales stand for, as `dtype`."""
-    n_in = _mx4_cols(codes, scales)
-    shape = codes.shape[:-1] + (n_in,)
-    out = torch.empty(shape, dtype=dtype, device=codes.device) if out is None else out
-    _need(out, "out", shape)
-    dev = codes.device
-    _launch("awq_mx4_dequantize", dev, _dev(codes, "codes", torch.uint8), _on(dev, scales, "scales", torch.uint8),
-            out.numel() // max(n_in, 1), n_in, _on(dev, out, "out"), _dtype_code(out))
+    n_in, dev = _mx4_cols(codes, scales), codes.device
+    shape = (*codes.shape[:-1], n_in)
+    out = torch.empty(shape, dtype=dtype, device=dev) if out is None else _need(out, "out", shape)
+    _launch("awq_mx4_dequantize", dev, _ptr(codes, "codes", None, torch.uint8),
+            _ptr(scales, "scales", dev, torch.uint8), math.prod(shape[:-1]), n_in, _ptr(out, "out", dev),
+            _dtype_code(out))
     return out
 
 
@@ -443,10 +448,9 @@ def mx4_gemm(X, codes, scales, y=None, y_f32=False):
         raise ValueError("codes must be (out, in / 2) for X (M, in)")
     out, dev = codes.shape[0], X.device
     ydt = torch.float32 if y_f32 else X.dtype
-    y = torch.empty((M, out), dtype=ydt, device=dev) if y is None else y
-    _need(y, "y", (M, out))
-    _launch("awq_mx4_gemm", dev, _dev(X, "X"), _dtype_code(X), M, n_in, _on(dev, codes, "codes", torch.uint8),
-            _on(dev, scales, "scales", torch.uint8), out, _on(dev, y, "y", ydt), _DTYPE[ydt])
+    y = torch.empty((M, out), dtype=ydt, device=dev) if y is None else _need(y, "y", (M, out))
+    _launch("awq_mx4_gemm", dev, _ptr(X, "X"), _dtype_code(X), M, n_in, _ptr(codes, "codes", dev, torch.uint8),
+            _ptr(scales, "scales", dev, torch.uint8), out, _ptr(y, "y", dev, ydt), _DTYPE[ydt])
     return y
 
 
@@ -457,16 +461,15 @@ def mx4_gemm_a4(x_codes, x_scales, codes, scales, dtype=torch.bfloat16, y=None):
     if x_codes.dim() != 2 or codes.dim() != 2 or _mx4_cols(codes, scales) != n_in:
         raise ValueError("x_codes must be (M, in / 2) and codes (out, in / 2)")
     M, out, dev = x_codes.shape[0], codes.shape[0], x_codes.device
-    y = torch.empty((M, out), dtype=dtype, device=dev) if y is None else y
-    _need(y, "y", (M, out))
-    _launch("awq_mx4_gemm_a4", dev, _dev(x_codes, "x_codes", torch.uint8), _on(dev, x_scales, "x_scales", torch.uint8),
-            M, n_in, _on(dev, codes, "codes", torch.uint8), _on(dev, scales, "scales", torch.uint8), out,
-            _on(dev, y, "y", dtype), _dtype_code(y))
+    y = torch.empty((M, out), dtype=dtype, device=dev) if y is None else _need(y, "y", (M, out))
+    _launch("awq_mx4_gemm_a4", dev, _ptr(x_codes, "x_codes", None, torch.uint8),
+            _ptr(x_scales, "x_scales", dev, torch.uint8), M, n_in, _ptr(codes, "codes", dev, torch.uint8),
+            _ptr(scales, "scales", dev, torch.uint8), out, _ptr(y, "y", dev, dtype), _dtype_code(y))
     return y
 
 
-def mx4_moe_workspace_size(M, inter, top_k):
-    return int(lib().awq_mx4_moe_workspace_size(M, inter, top_k))
+def mx4_moe_workspace_size(M, hidden, inter, top_k):
+    return int(lib().awq_mx4_moe_workspace_size(M, hidden, inter, top_k))
 
 
 def mx4_moe(X, router, gate_up, gate_up_scales, down, down_scales, top_k, renorm=True, y=None, workspace=None):
@@ -483,14 +486,13 @@ def mx4_moe(X, router, gate_up, gate_up_scales, down, down_scales, top_k, renorm
     _need(router, "router", (experts, hidden))
     _need(gate_up, "gate_up", (experts, 2 * inter, hidden // 2))
     _need(down, "down", (experts, hidden, inter // 2))
-    dev = X.device
-    y = torch.empty_like(X) if y is None else y
-    _need(y, "y", (M, hidden))
-    ws = _workspace(mx4_moe_workspace_size(M, inter, top_k), dev, workspace)
-    _launch("awq_mx4_moe", dev, _dev(X, "X"), _dtype_code(X), M, hidden, inter, experts, top_k, int(bool(renorm)),
-            _on(dev, router, "router", X.dtype), _on(dev, gate_up, "gate_up", torch.uint8),
-            _on(dev, gate_up_scales, "gate_up_scales", torch.uint8), _on(dev, down, "down", torch.uint8),
-            _on(dev, down_scales, "down_scales", torch.uint8), _on(dev, y, "y", X.dtype), _on(dev, ws, "workspace"),
+    dev, u8 = X.device, torch.uint8
+    y = torch.empty_like(X) if y is None else _need(y, "y", (M, hidden))
+    ws = _workspace(mx4_moe_workspace_size(M, hidden, inter, top_k), dev, workspace)
+    _launch("awq_mx4_moe", dev, _ptr(X, "X"), _dtype_code(X), M, hidden, inter, experts, top_k, int(bool(renorm)),
+            _ptr(router, "router", dev, X.dtype), _ptr(gate_up, "gate_up", dev, u8),
+            _ptr(gate_up_scales, "gate_up_scales", dev, u8), _ptr(down, "down", dev, u8),
+            _ptr(down_scales, "down_scales", dev, u8), _ptr(y, "y", dev, X.dtype), _ptr(ws, "workspace", dev),
             ws.numel() * ws.element_size())
     return y
 

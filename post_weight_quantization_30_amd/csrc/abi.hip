@@ -460,7 +460,7 @@ int mx4_shape(int64_t rows, int64_t in)
 {
     if (rows < 1 || in < 1 || in % AWQ_MX4_BLOCK != 0 || rows > INT64_MAX / in)
         return AWQ_ERR_INVALID_ARG;
-    if (rows * in > (int64_t)1 << 43 || in > (int64_t)1 << 30)
+    if (rows * in > (int64_t)1 << 43 || in > (int64_t)1 << 28)
         return AWQ_ERR_UNSUPPORTED;
     return AWQ_OK;
 }
@@ -470,7 +470,7 @@ int mx4_gemm_shape(int64_t M, int64_t in, int64_t out)
     if (M < 1 || out < 1 || in < 1 || in % AWQ_MX4_BLOCK != 0 || out > INT64_MAX / in || M > INT64_MAX / in ||
         M > INT64_MAX / out)
         return AWQ_ERR_INVALID_ARG;
-    if (M > 65535LL * 32 || in > (int64_t)1 << 30 || (out + 15) / 16 > (int64_t)0x7fffffff)
+    if (M > 65535LL * 32 || in > (int64_t)1 << 28 || (out + 15) / 16 > (int64_t)0x7fffffff)
         return AWQ_ERR_UNSUPPORTED;
     return AWQ_OK;
 }
@@ -534,20 +534,21 @@ int awq_mx4_gemm_a4(const uint8_t *xcodes, const uint8_t *xscales, int64_t M, in
 
 namespace {
 
-int mx4_moe_shape(int64_t M, int64_t inter, int top_k)
+int mx4_moe_shape(int64_t M, int64_t hidden, int64_t inter, int top_k)
 {
-    if (M < 1 || top_k < 1 || inter < 1 || inter % AWQ_MX4_BLOCK != 0)
+    if (M < 1 || top_k < 1 || hidden < 1 || hidden % AWQ_MX4_BLOCK != 0 || inter < 1 || inter % AWQ_MX4_BLOCK != 0)
         return AWQ_ERR_INVALID_ARG;
-    if (M > AWQ_MX4_MOE_MAX_TOKENS || top_k > AWQ_MX4_MOE_MAX_TOPK || inter > (int64_t)1 << 20)
+    if (M > AWQ_MX4_MOE_MAX_TOKENS || top_k > AWQ_MX4_MOE_MAX_TOPK || hidden > (int64_t)1 << 20 ||
+        inter > (int64_t)1 << 20)
         return AWQ_ERR_UNSUPPORTED;
     return AWQ_OK;
 }
 
 }  // namespace
 
-size_t awq_mx4_moe_workspace_size(int64_t M, int64_t inter, int top_k)
+size_t awq_mx4_moe_workspace_size(int64_t M, int64_t hidden, int64_t inter, int top_k)
 {
-    return mx4_moe_shape(M, inter, top_k) == AWQ_OK ? awq::mx4_moe_ws_layout(M, inter, top_k).total : 0;
+    return mx4_moe_shape(M, hidden, inter, top_k) == AWQ_OK ? awq::mx4_moe_ws_layout(M, hidden, inter, top_k).total : 0;
 }
 
 int awq_mx4_moe(const void *X, int dtype, int64_t M, int64_t hidden, int64_t inter, int experts, int top_k, int renorm,
@@ -555,15 +556,15 @@ int awq_mx4_moe(const void *X, int dtype, int64_t M, int64_t hidden, int64_t int
                 const uint8_t *dn_scales, void *Y, void *ws, size_t ws_bytes, void *stream)
 {
     if (!X || !router || !gu_codes || !gu_scales || !dn_codes || !dn_scales || !Y || !valid_dtype(dtype) ||
-        hidden < 1 || hidden % AWQ_MX4_BLOCK != 0 || experts < 1 || top_k > experts)
+        experts < 1 || top_k > experts)
         return AWQ_ERR_INVALID_ARG;
-    int st = mx4_moe_shape(M, inter, top_k);
+    int st = mx4_moe_shape(M, hidden, inter, top_k);
     if (st != AWQ_OK)
         return st;
-    if (dtype == AWQ_F32 || experts > AWQ_MX4_MOE_MAX_EXPERTS || hidden > (int64_t)1 << 20 || !aligned16(X) ||
+    if (dtype == AWQ_F32 || experts > AWQ_MX4_MOE_MAX_EXPERTS || !aligned16(X) ||
         !aligned16(router) || !aligned16(gu_codes) || !aligned16(dn_codes))
         return AWQ_ERR_UNSUPPORTED;
-    if (!ws || ws_bytes < awq::mx4_moe_ws_layout(M, inter, top_k).total)
+    if (!ws || ws_bytes < awq::mx4_moe_ws_layout(M, hidden, inter, top_k).total)
         return AWQ_ERR_WORKSPACE;
     if (!aligned16(ws))
         return AWQ_ERR_UNSUPPORTED;

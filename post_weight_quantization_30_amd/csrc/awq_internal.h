@@ -304,19 +304,32 @@ hipError_t launch_mx4_gemm(const void *X, int dtype, int64_t M, int64_t in, cons
 hipError_t launch_mx4_gemm_a4(const uint8_t *xcodes, const uint8_t *xscales, int64_t M, int64_t in,
                               const uint8_t *codes, const uint8_t *scales, int64_t out, void *Y, int y_dtype,
                               hipStream_t st);
+// Parts that the down product's contraction is shared out to: with fewer than
+// 256 tiles of 16 hidden columns as many as keep every unit busy, but no part
+// without 16 waves' worth of 512-column units (`routed`: experts at most).
+inline int mx4_moe_parts(int64_t hidden, int64_t inter, int64_t routed)
+{
+    const int64_t fill = 256 / (hidden / 16), work = routed * ((inter + 511) / 512) / 32;
+    const int64_t z = fill < work ? fill : work;
+    return (int)(z < 1 ? 1 : z > 8 ? 8 : z);
+}
 // Workspace of awq_mx4_moe: the routed experts and their weights, (M, top_k),
-// and p h of every pair, (M top_k, inter) in the activations' type.
+// p h of every pair, (M top_k, inter) in the activations' type, the logits and
+// the parts' fp32 sums.
 struct Mx4MoeWs {
-    size_t ids_off, w_off, h_off, total;
+    size_t ids_off, w_off, h_off, logits_off, sums_off, total;
 };
-inline Mx4MoeWs mx4_moe_ws_layout(int64_t M, int64_t inter, int top_k)
+inline Mx4MoeWs mx4_moe_ws_layout(int64_t M, int64_t hidden, int64_t inter, int top_k)
 {
     Mx4MoeWs w;
     const size_t pairs = (size_t)(M * top_k);
+    const int parts = mx4_moe_parts(hidden, inter, M * top_k);      // at least those of any number of experts
     w.ids_off = 0;
     w.w_off = align256(pairs * sizeof(int32_t));
     w.h_off = w.w_off + align256(pairs * sizeof(float));
-    w.total = w.h_off + align256(pairs * (size_t)inter * 2);
+    w.logits_off = w.h_off + align256(pairs * (size_t)inter * 2);
+    w.sums_off = w.logits_off + align256((size_t)M * AWQ_MX4_MOE_MAX_EXPERTS * sizeof(float));
+    w.total = w.sums_off + (parts > 1 ? align256((size_t)parts * (size_t)(M * hidden) * sizeof(float)) : 0);
     return w;
 }
 hipError_t launch_mx4_moe(const void *X, int dtype, int M, int hidden, int inter, int experts, int top_k, int renorm,

@@ -90,6 +90,86 @@ hipError_t split(const void *X, const uint8_t *xs, int64_t M, int nb, const uint
 }
 
 // ---------------------------------------------------------------------------
+// Up to 16 tokens of 16-bit activations, more row tiles than the chip has
+// units for a whole block each. Block: 8 / S row tiles of 16, all columns, S
+// waves a tile; the activations go through LDS in chunks of kc blocks that all
+// waves share. Every wave streams its own weights (see StreamItem), the next
+// item in flight also across the chunks' barriers.
+template <typename TX, typename TY, int S>
+__global__ __launch_bounds__(512, 4) void k_mx4_gemv(const TX *__restrict__ X, int M, int nb, int kc,
+                                                     const uint8_t *__restrict__ codes,
+                                                     const uint8_t *__restrict__ scales, int64_t out,
+                                                     TY *__restrict__ Y)
+{
+    __shared__ __align__(16) uint8_t lds[kStreamLds + 16 * 16];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 15, c = lane >> 4, part = wave % S;
+    const int64_t n0 = ((int64_t)blockIdx.x * (8 / S) + wave / S) * 16;
+    const int64_t first = n0 < out ? n0 : out - 1;         // rows past the end load the last one: not stored
+    StreamRows<1> rows = {{codes + first * nb * 16}, {scales + first * nb}};
+    rows.lane((uint32_t)(first + r < out ? r : out - 1 - first), c, nb);
+    const int stride = kc * 64 + 16, row = (r < M ? r : M - 1) * stride + c * 16;
+    const int items = (nb + kStreamBlocks - 1) / kStreamBlocks, per = kc / kStreamBlocks;
+    bool bad = false;
+    f32x4 acc[1][1];
+
+    auto stage = [&](int i0) {                             // columns of items i0 ... i0 + per - 1
+        const int b0 = i0 * kStreamBlocks, len = (b0 + kc < nb ? kc : nb - b0) * 4;
+        for (int m = wave; m < M; m += 8)
+            for (int j = lane; j < len; j += 64)
+                *reinterpret_cast<u32x4 *>(lds + m * stride + j * 16) =
+                    *reinterpret_cast<const u32x4 *>(X + ((int64_t)m * nb + b0) * 32 + j * 8);
+    };
+    auto contract = [&]<bool WIDE>() {
+        acc[0][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+        StreamItem<1> it;
+        int i = part;                                      // the wave's items: part, part + S, ...
+        if (i < items)
+            stream_load(it, rows, i * kStreamBlocks, nb, c);
+#pragma unroll 1
+        for (int i0 = 0; i0 < items; i0 += per) {
+            if (i0)
+                __syncthreads();
+            stage(i0);
+            __syncthreads();
+            const int end = i0 + per < items ? i0 + per : items;
+#pragma unroll 1
+            for (; i < end; i += S) {
+                const TX *const x[1] = {(const TX *)(lds + row + (i - i0) * kStreamBlocks * 64)};
+                stream_compute<WIDE, true>(it, x, acc, nb - i * kStreamBlocks, 1, rows,
+                                     i + S < items ? (i + S) * kStreamBlocks : -1, nb, c, bad);
+            }
+        }
+    };
+    contract.template operator()<false>();
+    if constexpr (std::is_same<TX, f16>::value)
+        if (__syncthreads_or(bad))                         // scales that fp16 cannot hold
+            contract.template operator()<true>();
+    if constexpr (S > 1) {
+        f32x4 *const red = reinterpret_cast<f32x4 *>(lds);
+        __syncthreads();
+        red[threadIdx.x] = acc[0][0];
+        __syncthreads();
+        if (part)
+            return;
+#pragma unroll
+        for (int k = 1; k < S; ++k)
+            acc[0][0] += red[threadIdx.x + 64 * k];
+    }
+    store_tile<TX, TY>(Y, 4 * c, n0 + r, M, out, acc[0][0]);
+}
+
+template <typename TX, typename TY, int S>
+hipError_t gemv(const void *X, int M, int nb, const uint8_t *codes, const uint8_t *scales, int64_t out, void *Y,
+                hipStream_t st)
+{
+    const int64_t tiles = (out + 15) / 16;
+    k_mx4_gemv<TX, TY, S><<<dim3((uint32_t)((tiles + 8 / S - 1) / (8 / S))), 512, 0, st>>>(
+        (const TX *)X, M, nb, stream_chunk(M, nb), codes, scales, out, (TY *)Y);
+    return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
 // Many tokens: 32x32 matrix tiles.
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
@@ -460,6 +540,17 @@ template <typename TX, typename TY>
 hipError_t gemm(const void *X, const uint8_t *xs, int64_t M, int nb, const uint8_t *codes, const uint8_t *scales,
                 int64_t out, void *Y, hipStream_t st)
 {
+    if constexpr (!std::is_same<TX, Mx4Act>::value) {
+        // Enough row tiles for more than a block's worth a unit: few waves a
+        // tile (28672 rows of 4096, 4 tokens: S = 1, 2, 4, 8 take 16.4, 15.7,
+        // 17.9, 21.1 us; 12288 rows, 2 tokens: 14.4, 10.3, 9.7, 10.9).
+        const int64_t tiles = (out + 15) / 16;
+        if (M <= 16 && tiles >= 640) {
+            if (tiles >= 1280)
+                return gemv<TX, TY, 2>(X, (int)M, nb, codes, scales, out, Y, st);
+            return gemv<TX, TY, 4>(X, (int)M, nb, codes, scales, out, Y, st);
+        }
+    }
     if (M <= 16)
         return split<TX, TY, 1, 1, 4>(X, xs, M, nb, codes, scales, out, Y, st);
     if constexpr (std::is_same<TX, Mx4Act>::value) {

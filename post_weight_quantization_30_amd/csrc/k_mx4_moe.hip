@@ -15,353 +15,521 @@ namespace awq {
 
 namespace {
 
-constexpr int kMaxTok = AWQ_MX4_MOE_MAX_TOKENS, kMaxE = AWQ_MX4_MOE_MAX_EXPERTS;
+constexpr int kMaxTok = AWQ_MX4_MOE_MAX_TOKENS, kMaxK = AWQ_MX4_MOE_MAX_TOPK, kMaxE = AWQ_MX4_MOE_MAX_EXPERTS;
 
-// ---- routing --------------------------------------------------------------
-// Block: 16 tokens, 16 waves splitting the columns in steps of 32 (one
-// 16x16x32 step per 16 experts); then wave w ranks token w's logits.
-constexpr int kRouteWaves = 16;
-constexpr int kRouteET = 4;        // expert tiles of 16 summed at a time
+// ---- routing ----------------------------------------------------------------
+// Logits: a block per expert and TOK tokens, its four waves and their lanes
+// along the columns. (A router row is read in whole kilobytes: 16 rows of 64
+// bytes, as a matrix tile would read them, keep a load unit busy twice as long.)
+template <typename TX, int TOK>
+__global__ __launch_bounds__(256) void k_mx4_moe_logits(const TX *__restrict__ X, int M, int hidden,
+                                                        const TX *__restrict__ router, int E,
+                                                        float *__restrict__ logits)
+{
+    typedef typename Vec8<TX>::type vec;
+    __shared__ float part[4][TOK];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, e = blockIdx.x, m0 = blockIdx.y * TOK;
+    const TX *const w = router + (int64_t)e * hidden;
+    const TX *x[TOK];
+    float acc[TOK];
+#pragma unroll
+    for (int t = 0; t < TOK; ++t) {                    // past the last token: that one again
+        x[t] = X + (int64_t)(m0 + t < M ? m0 + t : M - 1) * hidden;
+        acc[t] = 0.f;
+    }
+    for (int j = threadIdx.x * 8; j < hidden; j += 2048) {
+        const vec wv = load8(w + j);
+        vec xv[TOK];
+#pragma unroll
+        for (int t = 0; t < TOK; ++t)
+            xv[t] = load8(x[t] + j);
+        float wf[8];
+        widen8<TX>(wv, wf);
+#pragma unroll
+        for (int t = 0; t < TOK; ++t) {
+            float xf[8];
+            widen8<TX>(xv[t], xf);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                acc[t] = fmaf(xf[i], wf[i], acc[t]);
+        }
+    }
+    // lanes of the two halves keep one half of the tokens each, and so on: then
+    // lane l holds token l / (64 / TOK)
+#pragma unroll
+    for (int n = TOK / 2, off = 32; off > 0; off >>= 1, n /= 2) {
+        if (n > 0) {
+            const bool up = lane & off;
+#pragma unroll
+            for (int t = 0; t < n; ++t) {
+                const float give = up ? acc[t] : acc[t + n];
+                acc[t] = (up ? acc[t + n] : acc[t]) + __shfl_xor(give, off);
+            }
+        } else {
+            acc[0] += __shfl_xor(acc[0], off);
+        }
+    }
+    if ((lane & (64 / TOK - 1)) == 0)
+        part[wave][lane / (64 / TOK)] = acc[0];
+    __syncthreads();
+    const int t = threadIdx.x;
+    if (t < TOK && m0 + t < M)
+        logits[(int64_t)(m0 + t) * E + e] = (part[0][t] + part[1][t]) + (part[2][t] + part[3][t]);
+}
 
+// Larger logits have larger keys; NaN the lowest, -0 ties with +0.
 __device__ __forceinline__ uint32_t ordered(float x)
 {
     const uint32_t u = __builtin_bit_cast(uint32_t, x);
     if ((u & 0x7FFFFFFFu) > 0x7F800000u)
-        return 0;                                          // NaN ranks lowest
-    const uint32_t z = (u << 1) == 0 ? 0 : u;              // -0 ties with +0
+        return 0;
+    const uint32_t z = (u << 1) == 0 ? 0 : u;
     return z & 0x80000000u ? ~z : z | 0x80000000u;
 }
 
-template <typename TX>
-__global__ __launch_bounds__(64 * kRouteWaves) void k_mx4_moe_route(const TX *__restrict__ X, int M, int hidden,
-                                                                    const TX *__restrict__ router, int E, int top_k,
-                                                                    int renorm, int32_t *__restrict__ ids,
-                                                                    float *__restrict__ weights)
+// One wave per token: an expert's place is the number of those ahead of it.
+__global__ __launch_bounds__(64) void k_mx4_moe_topk(const float *__restrict__ logits, int E, int top_k, int renorm,
+                                                     int32_t *__restrict__ ids, float *__restrict__ weights)
 {
-    typedef typename Vec8<TX>::type vec;
-    __shared__ f32x4 red[kRouteWaves * kRouteET * 64];     // 64 KB
-    __shared__ float logits[16][kMaxE];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int r = lane & 15, c = lane >> 4;
-    const int m0 = blockIdx.x * 16;
-    const TX *x = X + (int64_t)(m0 + r < M ? m0 + r : M - 1) * hidden + 8 * c;
-    const int steps = hidden / 32;
-    for (int e0 = 0; e0 < E; e0 += 16 * kRouteET) {
-        const TX *w[kRouteET];
-#pragma unroll
-        for (int t = 0; t < kRouteET; ++t) {
-            const int e = e0 + 16 * t + r;
-            w[t] = router + (int64_t)(e < E ? e : E - 1) * hidden + 8 * c;
-        }
-        f32x4 acc[kRouteET];
-#pragma unroll
-        for (int t = 0; t < kRouteET; ++t)
-            acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-        for (int s = wave; s < steps; s += kRouteWaves) {
-            const vec xv = load8(x + s * 32);
-#pragma unroll
-            for (int t = 0; t < kRouteET; ++t)
-                acc[t] = mx4_mfma(xv, load8(w[t] + s * 32), acc[t]);
-        }
-#pragma unroll
-        for (int t = 0; t < kRouteET; ++t)
-            red[(wave * kRouteET + t) * 64 + lane] = acc[t];
-        __syncthreads();
-        for (int idx = threadIdx.x; idx < kRouteET * 64; idx += 64 * kRouteWaves) {
-            f32x4 sum = red[idx];
-#pragma unroll
-            for (int k = 1; k < kRouteWaves; ++k)
-                sum += red[k * kRouteET * 64 + idx];
-            const int l = idx & 63, e = e0 + 16 * (idx / 64) + (l & 15);
-            if (e < E)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    logits[4 * (l >> 4) + i][e] = sum[i];
-        }
-        __syncthreads();
-    }
-    const int m = m0 + wave;
-    if (m >= M)
-        return;
-    // lane l ranks experts l, l + 64, ...: the largest (value, lowest index)
-    // wins a round and leaves
+    __shared__ __align__(16) uint32_t keys[kMaxE];
+    __shared__ float chosen[kMaxK];
+    __shared__ int chosen_id[kMaxK];
+    const int lane = threadIdx.x;
+    const int64_t m = blockIdx.x;
     float l[kMaxE / 64];
-    uint64_t key[kMaxE / 64];
 #pragma unroll
     for (int q = 0; q < kMaxE / 64; ++q) {
-        const int e = lane + 64 * q;
-        l[q] = e < E ? logits[wave][e] : 0.f;
-        key[q] = e < E ? (uint64_t)ordered(l[q]) << 32 | (uint32_t)(0xFFFF - e) : 0;
+        const int e = 64 * q + lane;
+        l[q] = e < E ? logits[m * E + e] : 0.f;
+        keys[e] = e < E ? ordered(l[q]) : 0;           // past the last expert: ahead of nobody
     }
-    float top = 0.f, sum = 0.f, mine = 0.f;
-    int my_id = 0;
-    for (int k = 0; k < top_k; ++k) {
-        uint64_t best = 0;
+    __syncthreads();
 #pragma unroll
-        for (int q = 0; q < kMaxE / 64; ++q)
-            best = key[q] > best ? key[q] : best;
-        for (int off = 32; off > 0; off >>= 1) {
-            const uint64_t o = __shfl_xor(best, off);
-            best = o > best ? o : best;
-        }
-        const int e = 0xFFFF - (int)(uint32_t)best;
+    for (int q = 0; q < kMaxE / 64; ++q) {
+        const int e = 64 * q + lane;
+        if (e < E) {
+            const uint32_t key = keys[e];
+            int rank = 0;
+            for (int j = 0; j < E; j += 4) {
+                const u32x4 k4 = *reinterpret_cast<const u32x4 *>(&keys[j]);
 #pragma unroll
-        for (int q = 0; q < kMaxE / 64; ++q)
-            if (key[q] == best)
-                key[q] = 0;
-        const float v = logits[wave][e];
-        if (k == 0)
-            top = v;
-        const float p = expf(v - top);
-        if (renorm)
-            sum += p;
-        if (lane == k) {
-            mine = p;
-            my_id = e;
+                for (int i = 0; i < 4; ++i)
+                    rank += k4[i] > key || (k4[i] == key && j + i < e) ? 1 : 0;
+            }
+            if (rank < top_k) {
+                chosen[rank] = l[q];
+                chosen_id[rank] = e;
+            }
         }
     }
-    if (!renorm) {
+    __syncthreads();
+    const float top = chosen[0];
+    float total = 0.f;
+    if (renorm) {
+        for (int k = 0; k < top_k; ++k)
+            total += expf(chosen[k] - top);
+    } else {
 #pragma unroll
         for (int q = 0; q < kMaxE / 64; ++q)
-            sum += lane + 64 * q < E ? expf(l[q] - top) : 0.f;
+            total += 64 * q + lane < E ? expf(l[q] - top) : 0.f;
         for (int off = 32; off > 0; off >>= 1)
-            sum += __shfl_xor(sum, off);
+            total += __shfl_xor(total, off);
     }
     if (lane < top_k) {
-        ids[m * top_k + lane] = my_id;
-        weights[m * top_k + lane] = mine / sum;
+        ids[m * top_k + lane] = chosen_id[lane];
+        weights[m * top_k + lane] = expf(chosen[lane] - top) / total;
     }
 }
 
-// The routed experts as bits, from all ids (every thread of the block calls it).
-__device__ __forceinline__ void routed_bits(const int32_t *ids, int pairs, uint32_t (&bits)[kMaxE / 32])
+// What a block of `up` or `down` makes of the routing's ids: of every expert the
+// tokens (bits) and where its pairs begin in the list of pairs by expert and
+// token; the routed experts in ascending order.
+struct Routed {
+    uint64_t tokens[kMaxE];
+    uint32_t sums[kMaxE / 64];
+    uint16_t first[kMaxE], pairs[kMaxTok * kMaxK];
+    uint8_t expert[kMaxE], of_pair[kMaxTok * kMaxK];
+    int active;
+};
+
+__device__ __forceinline__ void read_routing(Routed &rt, const int32_t *ids, int pairs, int top_k)
 {
-    if (threadIdx.x < kMaxE / 32)
-        bits[threadIdx.x] = 0;
+    const int t = threadIdx.x, lane = t & 63;
+    if (t < kMaxE)
+        rt.tokens[t] = 0;
     __syncthreads();
-    for (int p = threadIdx.x; p < pairs; p += blockDim.x)
-        atomicOr(&bits[ids[p] >> 5], 1u << (ids[p] & 31));
+    for (int p = t; p < pairs; p += blockDim.x)
+        atomicOr((unsigned long long *)&rt.tokens[ids[p]], 1ull << (p / top_k));   // any order gives the same bits
+    __syncthreads();
+    // prefix sums over the experts, one a thread: pairs below 65536, experts above
+    uint32_t own = 0, sum = 0;
+    if (t < kMaxE) {
+        const int n = __popcll(rt.tokens[t]);
+        own = sum = n ? 0x10000u + n : 0;
+        for (int off = 1; off < 64; off <<= 1) {
+            const uint32_t o = __shfl_up(sum, off);
+            sum += lane >= off ? o : 0;
+        }
+        if (lane == 63)
+            rt.sums[t >> 6] = sum;
+    }
+    __syncthreads();
+    if (t < kMaxE) {
+        for (int q = 0; q < t >> 6; ++q)
+            sum += rt.sums[q];
+        rt.first[t] = (uint16_t)(sum - own);
+        if (own)
+            rt.expert[(sum - own) >> 16] = (uint8_t)t;
+        if (t == kMaxE - 1)
+            rt.active = (int)(sum >> 16);
+    }
+    __syncthreads();
+    for (int p = t; p < pairs; p += blockDim.x) {
+        const int e = ids[p];
+        const int at = rt.first[e] + __popcll(rt.tokens[e] & ((1ull << (p / top_k)) - 1));
+        rt.pairs[at] = (uint16_t)p;
+        rt.of_pair[at] = (uint8_t)e;
+    }
     __syncthreads();
 }
 
 // ---- gate and up ------------------------------------------------------------
-// Block: 16 columns of one expert's intermediate (a tile of gate rows and one
-// of up rows), all tokens routed to it, the hidden columns split over 8 waves.
+// Block: 8 / S tiles of 16 columns of one expert's intermediate (16 gate rows
+// and 16 up rows each), blockIdx.z's sixteen of the tokens routed to the expert,
+// S waves a tile splitting the hidden columns. The tokens' activations lie in
+// LDS by chunks of kc blocks; every wave streams its weights (see StreamItem).
 constexpr int kUpWaves = 8;
 
-template <typename TX, int MT, int U>
-__device__ __forceinline__ void up_tokens(const TX *__restrict__ X, int nb, const uint8_t *const (&w)[2],
-                                          const uint8_t *const (&ws)[2], const uint16_t *list, int count, int top_k,
-                                          const float *__restrict__ weights, int inter, int col0, f32x4 *red,
-                                          TX *__restrict__ h, int lane, int wave)
+template <typename TX, int S>
+__global__ __launch_bounds__(64 * kUpWaves, 4) void k_mx4_moe_up(const TX *__restrict__ X, int pairs, int hidden,
+                                                                 int inter, int top_k,
+                                                                 const int32_t *__restrict__ ids,
+                                                                 const float *__restrict__ weights,
+                                                                 const uint8_t *__restrict__ codes,
+                                                                 const uint8_t *__restrict__ scales,
+                                                                 TX *__restrict__ h)
 {
-    const int r = lane & 15, c = lane >> 4;
-    Mx4Rows<TX, MT, 2> rows;
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-        rows.w[nt] = w[nt];
-        rows.ws[nt] = ws[nt];
-    }
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        const int t = 16 * mt + r;
-        rows.x[mt] = X + (int64_t)(list[t < count ? t : count - 1] / top_k) * nb * 32;
-        rows.xs[mt] = nullptr;
-    }
-    f32x4 acc[MT][2];
-    mx4_wave<TX, MT, 2, U>(rows, acc, wave * (4 * U), kUpWaves * (4 * U), nb, c);
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        __syncthreads();           // the previous tile's sums are read
-        red[(wave * 2 + 0) * 64 + lane] = acc[mt][0];
-        red[(wave * 2 + 1) * 64 + lane] = acc[mt][1];
-        __syncthreads();
-        // one thread per (token, column): f32 k of lane l is token 4 (l / 16) + k
-        if (threadIdx.x < 256) {
-            const int col = threadIdx.x & 15, t = threadIdx.x >> 4;
-            const float *g = reinterpret_cast<const float *>(red) + ((t >> 2) * 16 + col) * 4 + (t & 3);
-            float gate = 0.f, up = 0.f;
-#pragma unroll
-            for (int k = 0; k < kUpWaves; ++k) {
-                gate += g[k * 512];
-                up += g[k * 512 + 256];
-            }
-            const int tok = 16 * mt + t;
-            if (tok < count) {
-                const int pair = list[tok];
-                const float v = gate / (1.0f + expf(-gate)) * up * weights[pair];
-                h[(int64_t)pair * inter + col0 + col] = static_cast<TX>(v);
-            }
-        }
-    }
-}
-
-template <typename TX>
-__global__ __launch_bounds__(64 * kUpWaves) void k_mx4_moe_up(const TX *__restrict__ X, int pairs, int hidden,
-                                                              int inter, int top_k, const int32_t *__restrict__ ids,
-                                                              const float *__restrict__ weights,
-                                                              const uint8_t *__restrict__ codes,
-                                                              const uint8_t *__restrict__ scales, TX *__restrict__ h)
-{
-    __shared__ uint32_t bits[kMaxE / 32];
-    __shared__ uint16_t list[kMaxTok];
-    __shared__ int s_count;
-    __shared__ f32x4 red[kUpWaves * 2 * 64];
+    __shared__ Routed rt;
+    __shared__ __align__(16) uint8_t lds[kStreamLds + 16 * 16];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    routed_bits(ids, pairs, bits);
-    int e = -1, skip = blockIdx.y;
-    for (int q = 0; q < kMaxE / 32 && e < 0; ++q) {
-        uint32_t b = bits[q];
-        const int n = __popc(b);
-        if (skip >= n) {
-            skip -= n;
-            continue;
-        }
-        for (; skip > 0; --skip)
-            b &= b - 1;
-        e = 32 * q + __ffs(b) - 1;
-    }
-    if (e < 0)
+    read_routing(rt, ids, pairs, top_k);
+    if ((int)blockIdx.y >= rt.active)
         return;                    // fewer routed experts than blocks: the whole block leaves
-    if (wave == 0) {               // this expert's pairs in ascending order (a token has it once at most)
-        int n = 0;
-        for (int p0 = 0; p0 < pairs; p0 += 64) {
-            const bool in = p0 + lane < pairs && ids[p0 + lane] == e;
-            const uint64_t mask = __ballot(in);
-            if (in)
-                list[n + __popcll(mask & ((1ull << lane) - 1))] = (uint16_t)(p0 + lane);
-            n += __popcll(mask);
+    const int e = __builtin_amdgcn_readfirstlane(rt.expert[blockIdx.y]);
+    const int all = (int)__popcll(rt.tokens[e]), t0 = (int)blockIdx.z * 16;
+    if (t0 >= all)
+        return;
+    const int nb = hidden / kMxBlock, r = lane & 15, c = lane >> 4, part = wave % S;
+    const int col0 = ((int)blockIdx.x * (kUpWaves / S) + wave / S) * 16;
+    const int64_t row = (int64_t)e * 2 * inter + (col0 < inter ? col0 : 0);          // past the end: not stored
+    StreamRows<2> rows = {{codes + row * nb * 16, codes + (row + inter) * nb * 16},
+                          {scales + row * nb, scales + (row + inter) * nb}};
+    rows.lane(r, c, nb);
+    const int items = (nb + kStreamBlocks - 1) / kStreamBlocks;
+
+    const uint16_t *const list = rt.pairs + rt.first[e] + t0;
+    const int count = __builtin_amdgcn_readfirstlane(all - t0 < 16 ? all - t0 : 16);
+    const int kc = stream_chunk(count, nb), stride = kc * 64 + 16, per = kc / kStreamBlocks;
+    const int xrow = (r < count ? r : count - 1) * stride + c * 16;
+    bool bad = false;
+    f32x4 acc[1][2];
+    auto contract = [&]<bool WIDE>() {
+        mx4_zero(acc);
+        StreamItem<2> a, b;
+        int i = part;                              // the wave's items: part, part + S, ...
+        bool in_a = true;                          // item i is in a
+        if (i < items)
+            stream_load(a, rows, i * kStreamBlocks, nb, c);
+        for (int i0 = 0; i0 < items; i0 += per) {
+            __syncthreads();                       // the LDS is free
+            const int b0 = i0 * kStreamBlocks, len = (b0 + kc < nb ? kc : nb - b0) * 4;
+            for (int m = wave; m < count; m += kUpWaves) {
+                const TX *const x = X + ((int64_t)(list[m] / top_k) * nb + b0) * 32;
+                for (int j = lane; j < len; j += 64)
+                    *reinterpret_cast<u32x4 *>(lds + m * stride + j * 16) =
+                        *reinterpret_cast<const u32x4 *>(x + j * 8);
+            }
+            __syncthreads();
+            const int end = i0 + per < items ? i0 + per : items;
+            auto one = [&](StreamItem<2> &cur, StreamItem<2> &next) {
+                if (i + S < items)
+                    stream_load(next, rows, (i + S) * kStreamBlocks, nb, c);
+                const TX *const x[1] = {(const TX *)(lds + xrow + (i - i0) * kStreamBlocks * 64)};
+                stream_compute<WIDE, false>(cur, x, acc, nb - i * kStreamBlocks, 1, rows, -1, nb, c, bad);
+                i += S;
+            };
+            while (i < end) {
+                if (in_a) {
+                    one(a, b);
+                    in_a = false;
+                    if (i >= end)
+                        break;
+                }
+                one(b, a);
+                in_a = true;
+            }
         }
-        if (lane == 0)
-            s_count = n;
+    };
+    contract.template operator()<false>();
+    if constexpr (std::is_same<TX, f16>::value)
+        if (__syncthreads_or(bad))                 // scales that fp16 cannot hold
+            contract.template operator()<true>();
+
+    if constexpr (S > 1) {
+        f32x4 *const red = reinterpret_cast<f32x4 *>(lds);
+        __syncthreads();
+        red[threadIdx.x * 2] = acc[0][0];
+        red[threadIdx.x * 2 + 1] = acc[0][1];
+        __syncthreads();
+        if (part == 0) {
+#pragma unroll
+            for (int k = 1; k < S; ++k) {
+                acc[0][0] += red[(threadIdx.x + 64 * k) * 2];
+                acc[0][1] += red[(threadIdx.x + 64 * k) * 2 + 1];
+            }
+        }
     }
-    __syncthreads();
-    const int count = s_count, nb = hidden / kMxBlock, col0 = blockIdx.x * 16, r = lane & 15;
-    const int64_t row = (int64_t)e * 2 * inter + col0 + r;
-    const uint8_t *const w[2] = {codes + row * nb * 16, codes + (row + inter) * nb * 16};
-    const uint8_t *const ws[2] = {scales + row * nb, scales + (row + inter) * nb};
-    if (count <= 16)
-        up_tokens<TX, 1, 2>(X, nb, w, ws, list, count, top_k, weights, inter, col0, red, h, lane, wave);
-    else if (count <= 32)
-        up_tokens<TX, 2, 1>(X, nb, w, ws, list, count, top_k, weights, inter, col0, red, h, lane, wave);
-    else
-        up_tokens<TX, 4, 1>(X, nb, w, ws, list, count, top_k, weights, inter, col0, red, h, lane, wave);
+    if (part == 0 && col0 < inter) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (4 * c + k < count) {
+                const int pair = list[4 * c + k];
+                const float gate = acc[0][0][k], up = acc[0][1][k];
+                const float v = gate / (1.0f + expf(-gate)) * up * weights[pair];
+                h[(int64_t)pair * inter + col0 + r] = static_cast<TX>(v);
+            }
+        }
+    }
 }
 
 // ---- down -------------------------------------------------------------------
-// Block: 16 hidden columns, all tokens; the waves split (routed expert, 128 U
-// columns of it) items. A token that an expert does not serve multiplies some
-// other row and drops the result: a NaN scale of an expert reaches its own
-// tokens only.
-constexpr int kDownWaves = 8;
+// Block: 16 hidden columns, all tokens, 16 waves (8 for more than 16 tokens:
+// registers). The contraction is a list of units, 512 columns of one routed
+// expert each, by expert and column. A unit's activations are one row of 1 KB
+// for each token that the expert serves; a stage is as many units as have 64
+// rows at most, in one of two LDS buffers, and the waves take its units in turn.
+// A stage's rows are on their way to registers while the one before it is
+// multiplied, and so are every wave's next weights, across the stages'
+// barriers. A token that an expert does not serve multiplies some other row
+// and drops the result: an expert's NaN reaches its own tokens only. With few
+// hidden columns the units are shared out over gridDim.y blocks, whose fp32
+// sums k_mx4_moe_sum adds (`sums`: (gridDim.y, M, hidden)).
+constexpr int kRowBytes = 64 * kStreamBlocks + 16;     // of a row in LDS, padded (see stream_chunk)
+constexpr int kDownRows = 64;                          // of a stage
+template <int MT> constexpr int kDownWavesOf = MT == 1 ? 16 : 8;
 
-template <typename TX, int MT, int U>
-__global__ __launch_bounds__(64 * kDownWaves) void k_mx4_moe_down(const TX *__restrict__ h, int M, int hidden, int inter,
+template <typename TX, int MT>
+__global__ __launch_bounds__(64 * kDownWavesOf<MT>) void k_mx4_moe_down(const TX *__restrict__ h, int M, int hidden, int inter,
                                                                   int top_k, const int32_t *__restrict__ ids,
                                                                   const uint8_t *__restrict__ codes,
                                                                   const uint8_t *__restrict__ scales,
-                                                                  TX *__restrict__ Y)
+                                                                  TX *__restrict__ Y, float *__restrict__ sums)
 {
-    __shared__ uint32_t bits[kMaxE / 32];
-    __shared__ uint8_t expert[kMaxE];
-    __shared__ __align__(8) int16_t pair_of[kMaxE][16 * MT];       // (routed expert, token) -> pair or -1
-    __shared__ f32x4 red[kDownWaves * MT * 64];
+    constexpr int kWaves = kDownWavesOf<MT>;
+    constexpr int kRegs = kDownRows / kWaves;          // rows a wave moves in a stage
+    __shared__ __align__(16) uint8_t bufs[2][kDownRows * kRowBytes];
+    __shared__ Routed rt;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int r = lane & 15, c = lane >> 4, pairs = M * top_k;
-    routed_bits(ids, pairs, bits);
-    int active = 0;
-#pragma unroll
-    for (int q = 0; q < kMaxE / 32; ++q)
-        active += __popc(bits[q]);
-    for (int idx = threadIdx.x; idx < active * 16 * MT; idx += blockDim.x)
-        pair_of[idx / (16 * MT)][idx % (16 * MT)] = -1;
-    __syncthreads();
-    for (int p = threadIdx.x; p < pairs; p += blockDim.x) {
-        const int e = ids[p];
-        int a = __popc(bits[e >> 5] & ((1u << (e & 31)) - 1));
-        for (int q = 0; q < e >> 5; ++q)
-            a += __popc(bits[q]);
-        expert[a] = (uint8_t)e;                                    // the same value from every pair of e
-        pair_of[a][p / top_k] = (int16_t)p;
-    }
-    __syncthreads();
+    const int r = lane & 15, c = lane >> 4;
+    read_routing(rt, ids, M * top_k, top_k);
+    const int active = __builtin_amdgcn_readfirstlane(rt.active);
+    const int nb = inter / kMxBlock, per = (nb + kStreamBlocks - 1) / kStreamBlocks;   // units of an expert
 
-    const int nb = inter / kMxBlock, per = (nb + 4 * U - 1) / (4 * U), items = active * per;
-    const int n = blockIdx.x * 16 + r;
-    f32x4 acc[MT][1];
-    bool bad = false;
-    mx4_zero(acc);
-
-    auto load = [&](Mx4Item<TX, MT, 1, U> &it, int i) {
-        const int a = i / per, b0 = (i - a * per) * 4 * U;
-        const int64_t row = (int64_t)expert[a] * hidden + n;
-        Mx4Rows<TX, MT, 1> rows;
-        rows.w[0] = codes + row * nb * 16;
-        rows.ws[0] = scales + row * nb;
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            const int p = pair_of[a][16 * mt + r];
-            rows.x[mt] = h + (int64_t)(p < 0 ? 0 : p) * inter;
-            rows.xs[mt] = nullptr;
-        }
-        mx4_load(it, rows, b0, nb, c);
+    // Rows in unit order: expert e's begin at per * first[e], unit i's at
+    // + i * count. A stage: units u0 ... u0 + units - 1, rows r0 ... r0 + rows - 1.
+    struct Stage {                                     // uniform
+        int u0, units, r0, rows;
     };
-    auto compute = [&]<bool WIDE>(Mx4Item<TX, MT, 1, U> &it, int i) {
-        const int a = i / per, b0 = (i - a * per) * 4 * U;
-        f32x4 part[MT][1];
-        mx4_zero(part);
-        mx4_compute<WIDE>(it, part, b0, nb, c, bad);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (pair_of[a][16 * mt + 4 * c + k] >= 0)
-                    acc[mt][0][k] += part[mt][0][k];
-    };
-    Mx4Item<TX, MT, 1, U> A, B;
-    int i = wave;
-    if (i < items) {
-        load(A, i);
-        while (true) {
-            if (i + kDownWaves < items)
-                load(B, i + kDownWaves);
-            compute.template operator()<false>(A, i);
-            i += kDownWaves;
-            if (i >= items)
-                break;
-            if (i + kDownWaves < items)
-                load(A, i + kDownWaves);
-            compute.template operator()<false>(B, i);
-            i += kDownWaves;
-            if (i >= items)
-                break;
+    const int first_unit = (int)((int64_t)per * active * blockIdx.y / gridDim.y);
+    const int end_unit = (int)((int64_t)per * active * (blockIdx.y + 1) / gridDim.y);
+    auto open = [&](Stage &s, int u0) {
+        s.u0 = u0;
+        s.units = s.rows = s.r0 = 0;
+        if (u0 >= end_unit)
+            return;
+        const int rank = u0 / per, i = u0 - rank * per;
+        const int e = rt.expert[rank];
+        const int count = __builtin_amdgcn_readfirstlane(__popcll(rt.tokens[e]));
+        s.r0 = __builtin_amdgcn_readfirstlane(per * rt.first[e]) + i * count;
+        const int left = per - i, fit = kDownRows / count;
+        if (fit < left) {                              // ends inside this expert
+            s.units = fit < end_unit - u0 ? fit : end_unit - u0;
+            s.rows = s.units * count;
+            return;
         }
-        if constexpr (std::is_same<TX, f16>::value) {
-            if (__any(bad)) {          // scales that fp16 cannot hold: once more in the wide form
-                mx4_zero(acc);
-#pragma unroll 1
-                for (i = wave; i < items; i += kDownWaves) {
-                    load(A, i);
-                    compute.template operator()<true>(A, i);
-                }
+        // lane l: whether the stage holds all of the experts up to rank + l
+        const int k = rank + lane < active ? rt.expert[rank + lane] : e;
+        const int end = per * (rt.first[k] + (int)__popcll(rt.tokens[k])) - s.r0;
+        const uint64_t whole = __ballot(rank + lane < active && end <= kDownRows);
+        const int n = __popcll(whole);                 // a run from lane 0 on: ends only grow
+        const int used = __builtin_amdgcn_readfirstlane(__shfl(end, n - 1));
+        s.units = left + (n - 1) * per;
+        s.rows = used;
+        if (rank + n < active) {                       // and some units of the next
+            const int cnt = __builtin_amdgcn_readfirstlane(__popcll(rt.tokens[rt.expert[rank + n]]));
+            const int more = (kDownRows - used) / cnt;
+            s.units += more < per ? more : per - 1;
+            s.rows += (more < per ? more : per - 1) * cnt;
+        }
+        if (s.units > end_unit - u0)                   // the rows past the last unit are moved, not used
+            s.units = end_unit - u0;
+    };
+    u32x4 pre[kRegs];
+    auto row_source = [&](const Stage &s, int q, int &chunks) -> const TX * {
+        const int R = s.r0 + wave + q * kWaves, at = R / per;      // `at` lies in the expert's pairs
+        const int e = rt.of_pair[at], first = rt.first[e], count = (int)__popcll(rt.tokens[e]);
+        const int local = R - per * first, i = local / count, p = rt.pairs[first + local - i * count];
+        chunks = (nb - i * kStreamBlocks < kStreamBlocks ? nb - i * kStreamBlocks : kStreamBlocks) * 4;
+        return h + ((int64_t)p * nb + i * kStreamBlocks) * 32;
+    };
+    auto fetch = [&](const Stage &s) {
+#pragma unroll
+        for (int q = 0; q < kRegs; ++q)
+            if (wave + q * kWaves < s.rows) {
+                int chunks;
+                const TX *const src = row_source(s, q, chunks);
+                if (lane < chunks)
+                    pre[q] = *reinterpret_cast<const u32x4 *>(src + lane * 8);
             }
+    };
+    auto stash = [&](const Stage &s, uint8_t *buf) {   // lanes past a row's end store what nothing reads
+#pragma unroll
+        for (int q = 0; q < kRegs; ++q)
+            if (wave + q * kWaves < s.rows)
+                *reinterpret_cast<u32x4 *>(buf + (wave + q * kWaves) * kRowBytes + lane * 16) = pre[q];
+    };
+    StreamRows<1> rows;
+    rows.lane(r, c, nb);
+    auto aim = [&](int u) -> int {                     // rows of the unit's expert; the unit's first block
+        const int rank = u / per;
+        const int64_t row = (int64_t)__builtin_amdgcn_readfirstlane(rt.expert[rank]) * hidden + blockIdx.x * 16;
+        rows.w[0] = codes + row * nb * 16;
+        rows.s[0] = scales + row * nb;
+        return (u - rank * per) * kStreamBlocks;
+    };
+    bool bad = false;
+    f32x4 acc[MT][1];
+
+    auto contract = [&]<bool WIDE>() {
+        mx4_zero(acc);
+        Stage cur, nxt;
+        open(cur, first_unit);
+        fetch(cur);
+        StreamItem<1> it;                              // the wave's next unit, if `loaded`
+        bool loaded = wave < cur.units;
+        if (loaded)
+            stream_load(it, rows, aim(first_unit + wave), nb, c);
+        stash(cur, bufs[0]);
+        open(nxt, cur.u0 + cur.units);
+        fetch(nxt);
+        __syncthreads();
+        uint8_t *now = bufs[0], *then = bufs[1];
+#pragma unroll 1
+        while (cur.units) {
+#pragma unroll 1
+            for (int j = wave; j < cur.units; j += kWaves) {
+                const int u = cur.u0 + j, rank = u / per, i = u - rank * per;
+                const int e = __builtin_amdgcn_readfirstlane(rt.expert[rank]);
+                const uint64_t set = rt.tokens[e];
+                const int count = (int)__popcll(set), row0 = per * rt.first[e] + i * count - cur.r0;
+                const TX *x[MT];
+                int tiles = 0;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    const int tok = 16 * mt + r, pos = (int)__popcll(set & ((1ull << tok) - 1));
+                    x[mt] = (const TX *)(now + (row0 + (pos < count ? pos : count - 1)) * kRowBytes + c * 16);
+                    tiles |= (set >> (16 * mt) & 0xFFFF ? 1 : 0) << mt;
+                }
+                tiles = __builtin_amdgcn_readfirstlane(tiles);
+                const int ahead = j + kWaves < cur.units ? cur.u0 + j + kWaves : wave < nxt.units ? nxt.u0 + wave : -1;
+                loaded = ahead >= 0;
+                const int next_b0 = loaded ? aim(ahead) : -1;
+                const TX *const(&xr)[MT] = x;
+                f32x4 part[MT][1];
+                mx4_zero(part);
+                stream_compute<WIDE, true>(it, xr, part, nb - i * kStreamBlocks, tiles, rows, next_b0, nb, c, bad);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        acc[mt][0][k] += set >> (16 * mt + 4 * c + k) & 1 ? part[mt][0][k] : 0.0f;
+            }
+            if (!loaded && wave < nxt.units) {         // nothing was left for it in this stage
+                loaded = true;
+                stream_load(it, rows, aim(nxt.u0 + wave), nb, c);
+            }
+            stash(nxt, then);
+            cur = nxt;
+            open(nxt, cur.u0 + cur.units);
+            fetch(nxt);
+            __syncthreads();
+            uint8_t *const t = now;
+            now = then;
+            then = t;
         }
-    }
+    };
+    contract.template operator()<false>();
+    if constexpr (std::is_same<TX, f16>::value)
+        if (__syncthreads_or(bad))                     // scales that fp16 cannot hold
+            contract.template operator()<true>();
+
+    f32x4 *const red = reinterpret_cast<f32x4 *>(bufs[0]);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
         red[(wave * MT + mt) * 64 + lane] = acc[mt][0];
     __syncthreads();
-    for (int idx = threadIdx.x; idx < MT * 64; idx += 64 * kDownWaves) {
+    for (int idx = threadIdx.x; idx < MT * 64; idx += 64 * kWaves) {
         f32x4 sum = red[idx];
 #pragma unroll
-        for (int w = 1; w < kDownWaves; ++w)
+        for (int w = 1; w < kWaves; ++w)
             sum += red[w * MT * 64 + idx];
         const int l = idx & 63, m = 16 * (idx / 64) + 4 * (l >> 4);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            if (m + k < M)
-                Y[(int64_t)(m + k) * hidden + blockIdx.x * 16 + (l & 15)] = static_cast<TX>(sum[k]);
+            if (m + k < M) {
+                const int64_t at = (int64_t)(m + k) * hidden + blockIdx.x * 16 + (l & 15);
+                if (gridDim.y > 1)
+                    sums[blockIdx.y * (int64_t)M * hidden + at] = sum[k];
+                else
+                    Y[at] = static_cast<TX>(sum[k]);
+            }
     }
+}
+
+// Y = the sum of Z parts of n fp32 values, in order.
+template <typename TX>
+__global__ __launch_bounds__(256) void k_mx4_moe_sum(const float *__restrict__ sums, int n, int Z, TX *__restrict__ Y)
+{
+    const int i = blockIdx.x * 256 + threadIdx.x;
+    if (i >= n)
+        return;
+    float v = sums[i];
+    for (int z = 1; z < Z; ++z)
+        v += sums[(int64_t)z * n + i];
+    Y[i] = static_cast<TX>(v);
+}
+
+template <typename TX, int TOK>
+void logits(const TX *X, int M, int hidden, const TX *router, int E, float *out, hipStream_t st)
+{
+    k_mx4_moe_logits<TX, TOK><<<dim3(E, (M + TOK - 1) / TOK), 256, 0, st>>>(X, M, hidden, router, E, out);
+}
+
+template <typename TX, int S>
+void up(const TX *X, int pairs, int most, int hidden, int inter, int top_k, const int32_t *ids, const float *weights,
+        const uint8_t *gu, const uint8_t *gus, TX *h, hipStream_t st)
+{
+    const int tiles = inter / 16, per = kUpWaves / S;
+    k_mx4_moe_up<TX, S><<<dim3((tiles + per - 1) / per, most, (pairs / top_k + 15) / 16), 64 * kUpWaves, 0, st>>>(
+        X, pairs, hidden, inter, top_k, ids, weights, gu, gus, h);
+}
+
+template <typename TX, int MT>
+void down(int Z, const TX *h, int M, int hidden, int inter, int top_k, const int32_t *ids, const uint8_t *dn,
+          const uint8_t *dns, TX *Y, float *sums, hipStream_t st)
+{
+    k_mx4_moe_down<TX, MT><<<dim3(hidden / 16, Z), 64 * kDownWavesOf<MT>, 0, st>>>(h, M, hidden, inter, top_k, ids, dn,
+                                                                                  dns, Y, sums);
 }
 
 template <typename TX>
@@ -369,22 +537,39 @@ hipError_t moe(const void *X, int M, int hidden, int inter, int E, int top_k, in
                const uint8_t *gu, const uint8_t *gus, const uint8_t *dn, const uint8_t *dns, void *Y, char *ws,
                hipStream_t st)
 {
-    const Mx4MoeWs lay = mx4_moe_ws_layout(M, inter, top_k);
-    int32_t *ids = (int32_t *)(ws + lay.ids_off);
-    float *weights = (float *)(ws + lay.w_off);
-    TX *h = (TX *)(ws + lay.h_off);
-    const int pairs = M * top_k;
-    k_mx4_moe_route<TX><<<dim3((M + 15) / 16), 64 * kRouteWaves, 0, st>>>(
-        (const TX *)X, M, hidden, (const TX *)router, E, top_k, renorm, ids, weights);
-    k_mx4_moe_up<TX><<<dim3(inter / 16, pairs < E ? pairs : E), 64 * kUpWaves, 0, st>>>(
-        (const TX *)X, pairs, hidden, inter, top_k, ids, weights, gu, gus, h);
-    const dim3 grid(hidden / 16), block(64 * kDownWaves);
-    if (M <= 16)
-        k_mx4_moe_down<TX, 1, 4><<<grid, block, 0, st>>>(h, M, hidden, inter, top_k, ids, dn, dns, (TX *)Y);
-    else if (M <= 32)
-        k_mx4_moe_down<TX, 2, 2><<<grid, block, 0, st>>>(h, M, hidden, inter, top_k, ids, dn, dns, (TX *)Y);
+    const Mx4MoeWs lay = mx4_moe_ws_layout(M, hidden, inter, top_k);
+    int32_t *const ids = (int32_t *)(ws + lay.ids_off);
+    float *const weights = (float *)(ws + lay.w_off), *const lg = (float *)(ws + lay.logits_off);
+    float *const sums = (float *)(ws + lay.sums_off);
+    TX *const h = (TX *)(ws + lay.h_off);
+    const TX *const x = (const TX *)X, *const rw = (const TX *)router;
+    const int pairs = M * top_k, most = pairs < E ? pairs : E;     // routed experts at most
+    if (M == 1)
+        logits<TX, 1>(x, M, hidden, rw, E, lg, st);
+    else if (M <= 4)
+        logits<TX, 4>(x, M, hidden, rw, E, lg, st);
     else
-        k_mx4_moe_down<TX, 4, 1><<<grid, block, 0, st>>>(h, M, hidden, inter, top_k, ids, dn, dns, (TX *)Y);
+        logits<TX, 8>(x, M, hidden, rw, E, lg, st);
+    k_mx4_moe_topk<<<dim3(M), 64, 0, st>>>(lg, E, top_k, renorm, ids, weights);
+    // waves a tile: as few as leave about two blocks a unit
+    const int64_t tiles = (int64_t)(inter / 16) * most;
+    if (tiles >= 2048)
+        up<TX, 1>(x, pairs, most, hidden, inter, top_k, ids, weights, gu, gus, h, st);
+    else if (tiles >= 1536)
+        up<TX, 2>(x, pairs, most, hidden, inter, top_k, ids, weights, gu, gus, h, st);
+    else if (tiles >= 768)
+        up<TX, 4>(x, pairs, most, hidden, inter, top_k, ids, weights, gu, gus, h, st);
+    else
+        up<TX, 8>(x, pairs, most, hidden, inter, top_k, ids, weights, gu, gus, h, st);
+    const int Z = mx4_moe_parts(hidden, inter, most);
+    if (M <= 16)
+        down<TX, 1>(Z, h, M, hidden, inter, top_k, ids, dn, dns, (TX *)Y, sums, st);
+    else if (M <= 32)
+        down<TX, 2>(Z, h, M, hidden, inter, top_k, ids, dn, dns, (TX *)Y, sums, st);
+    else
+        down<TX, 4>(Z, h, M, hidden, inter, top_k, ids, dn, dns, (TX *)Y, sums, st);
+    if (Z > 1)
+        k_mx4_moe_sum<TX><<<dim3((M * hidden + 255) / 256), 256, 0, st>>>(sums, M * hidden, Z, (TX *)Y);
     return hipGetLastError();
 }
 

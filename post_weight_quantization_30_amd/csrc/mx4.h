@@ -5,11 +5,15 @@
 // e8m0 byte: value = e2m1(code) * 2^(byte - 127), byte 255 = NaN. A row has
 // nb = in / 32 blocks, so its codes are 16 nb bytes and its scales nb bytes.
 //
-// The products below read both operands in whole blocks: in a 16-row matrix
-// tile lane (r, c) = (lane % 16, lane / 16) holds block 4u + c of row r in
-// step u. The sum over columns does not depend on the order in which both
-// operands present them, so no operand is rearranged: a lane's block is one
-// 16-byte load of codes and, for 16-bit activations, 64 contiguous bytes.
+// The products read weights in whole blocks: in a 16-row matrix tile lane
+// (r, c) = (lane % 16, lane / 16) loads block 4u + c of row r, 16 bytes. The
+// matrix step for 32 columns wants columns 8c ... 8c + 7 of one block in lane
+// c: the four words of four lanes are transposed (transpose4), so that step s
+// is block 4u + s for weights and 16-bit activations alike, and a load of
+// activations is 64 contiguous bytes a row. With the words left where they
+// are, lane c would want block 4u + c of the activations: a load would touch
+// twice the cache lines for 16 bytes each, which held a decode product of 16
+// tokens at a third of the speed.
 #pragma once
 
 #include <type_traits>
@@ -76,6 +80,18 @@ __device__ __forceinline__ void split_f16(const f16x8 &x, bf16x8 &hi, bf16x8 &lo
     }
 }
 
+// Word s of lane c <-> word c of lane s, for the four lanes (r, 0..3) of every
+// row: two swaps of half waves, two of quarter waves.
+__device__ __forceinline__ void transpose4(u32x4 &w)
+{
+    typedef uint32_t pair __attribute__((ext_vector_type(2)));
+    const pair a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+    const pair b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+    const pair c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+    const pair d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+    w = u32x4{c[0], c[1], d[0], d[1]};
+}
+
 __device__ __forceinline__ f32x4 mx4_mfma(const bf16x8 &a, const bf16x8 &b, const f32x4 &c)
 {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
@@ -97,9 +113,23 @@ __device__ __forceinline__ f32x4 mx4_mfma(const u32x4 &a, uint32_t sa, const u32
 // and 16 MT activation rows.
 template <typename TX, int MT, int NT, int U> struct Mx4Item {
     u32x4 w[NT][U];
-    uint32_t ws[NT][U];
+    uint32_t ws[NT][U];            // the four blocks' scale bytes
     XFrag<TX> x[MT][U];
 };
+
+// The scale bytes of blocks b .. b + 3 of a row (127 for those past its end).
+__device__ __forceinline__ uint32_t mx4_scales4(const uint8_t *row, int b, int nb)
+{
+    uint32_t v;
+    if (b + 4 <= nb) {
+        __builtin_memcpy(&v, row + b, 4);              // at any alignment
+    } else {
+        v = 0x7F7F7F7Fu;
+        for (int i = 0; b + i < nb; ++i)
+            v = (v & ~(0xFFu << (8 * i))) | (uint32_t)row[b + i] << (8 * i);
+    }
+    return v;
+}
 
 // A lane's rows: pointers to the starts of their codes, scales and activations.
 template <typename TX, int MT, int NT> struct Mx4Rows {
@@ -116,102 +146,101 @@ __device__ __forceinline__ void mx4_load(Mx4Item<TX, MT, NT, U> &it, const Mx4Ro
 {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        int b = b0 + 4 * u + c;
-        b = b < nb ? b : nb - 1;
+        const int b4 = b0 + 4 * u, b = b4 + c < nb ? b4 + c : nb - 1;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             it.w[nt][u] = *reinterpret_cast<const u32x4 *>(rows.w[nt] + (int64_t)b * 16);
-            it.ws[nt][u] = rows.ws[nt][b];
+            it.ws[nt][u] = mx4_scales4(rows.ws[nt], b4, nb);
         }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             if constexpr (std::is_same<TX, Mx4Act>::value) {
                 it.x[mt][u].q = *reinterpret_cast<const u32x4 *>((const uint8_t *)rows.x[mt] + (int64_t)b * 16);
-                it.x[mt][u].s = rows.xs[mt][b];
+                it.x[mt][u].s = mx4_scales4(rows.xs[mt], b4, nb);
             } else {
-                const TX *p = (const TX *)rows.x[mt] + (int64_t)b * 32;
 #pragma unroll
-                for (int s = 0; s < 4; ++s)
-                    it.x[mt][u].v[s] = load8(p + 8 * s);
+                for (int s = 0; s < 4; ++s) {
+                    const int bs = b4 + s < nb ? b4 + s : nb - 1;
+                    it.x[mt][u].v[s] = load8((const TX *)rows.x[mt] + (int64_t)bs * 32 + 8 * c);
+                }
             }
         }
     }
 }
 
-// acc += the item's products. A lane whose block lies past the row's end
-// multiplies zeros (its weights are then finite: scale 1). WIDE is for fp16
-// activations under scales that fp16 cannot hold: weights in bf16, activations
-// as two bf16 parts. The plain form reports such scales in `bad`.
+// acc += the item's products. Blocks past the row's end: their steps are left
+// out (16-bit activations), or zeros under scale 1 multiply (MXFP4). WIDE is
+// for fp16 activations under scales that fp16 cannot hold: weights in bf16,
+// activations as two bf16 parts. The plain form reports such scales in `bad`.
 template <bool WIDE, typename TX, int MT, int NT, int U>
 __device__ __forceinline__ void mx4_compute(Mx4Item<TX, MT, NT, U> &it, f32x4 (&acc)[MT][NT], int b0, int nb, int c,
                                             bool &bad)
 {
-    if (b0 + 4 * U > nb) {
+    if constexpr (std::is_same<TX, Mx4Act>::value) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (b0 + 4 * u + c < nb)
-                continue;
+            if (b0 + 4 * u + 4 > nb && b0 + 4 * u + c >= nb) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    it.w[nt][u] = u32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                    it.x[mt][u].q = u32x4{0, 0, 0, 0};
+            }
+            uint32_t sx[MT];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+                sx[mt] = it.x[mt][u].s >> (8 * c);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const uint32_t sw = it.ws[nt][u] >> (8 * c);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                    acc[mt][nt] = mx4_mfma(it.x[mt][u].q, sx[mt], it.w[nt][u], sw, acc[mt][nt]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-                it.ws[nt][u] = 127;
+                transpose4(it.w[nt][u]);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                if constexpr (std::is_same<TX, Mx4Act>::value) {
-                    it.x[mt][u].q = u32x4{0, 0, 0, 0};
-                    it.x[mt][u].s = 127;
+            for (int s = 0; s < 4; ++s) {
+                if (b0 + 4 * u + s >= nb)
+                    break;
+                if constexpr (!WIDE) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const uint32_t byte = it.ws[nt][u] >> (8 * s) & 0xFFu;
+                        typename Vec8<TX>::type w;
+                        if constexpr (std::is_same<TX, f16>::value) {
+                            w = mx4_to_f16(it.w[nt][u][s], mx4_scale(byte));
+                            bad = bad || !mx4_fits_f16(byte);
+                        } else {
+                            w = mx4_to_bf16(it.w[nt][u][s], mx4_scale(byte));
+                        }
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt)
+                            acc[mt][nt] = mx4_mfma(it.x[mt][u].v[s], w, acc[mt][nt]);
+                    }
                 } else {
 #pragma unroll
-                    for (int s = 0; s < 4; ++s)
-                        it.x[mt][u].v[s] = typename Vec8<TX>::type{};
+                    for (int mt = 0; mt < MT; ++mt) {
+                        __builtin_amdgcn_sched_barrier(0);   // one split at a time: registers
+                        bf16x8 hi, lo;
+                        split_f16(it.x[mt][u].v[s], hi, lo);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const bf16x8 w =
+                                mx4_to_bf16(it.w[nt][u][s], mx4_scale(it.ws[nt][u] >> (8 * s) & 0xFFu));
+                            acc[mt][nt] = mx4_mfma(hi, w, acc[mt][nt]);
+                            acc[mt][nt] = mx4_mfma(lo, w, acc[mt][nt]);
+                        }
+                    }
                 }
             }
         }
-    }
-    if constexpr (std::is_same<TX, Mx4Act>::value) {
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    acc[mt][nt] = mx4_mfma(it.x[mt][u].q, it.x[mt][u].s, it.w[nt][u], it.ws[nt][u], acc[mt][nt]);
-    } else if constexpr (!WIDE) {
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const float s = mx4_scale(it.ws[nt][u]);
-                if constexpr (std::is_same<TX, f16>::value)
-                    bad = bad || !mx4_fits_f16(it.ws[nt][u]);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    typename Vec8<TX>::type w;
-                    if constexpr (std::is_same<TX, f16>::value)
-                        w = mx4_to_f16(it.w[nt][u][k], s);
-                    else
-                        w = mx4_to_bf16(it.w[nt][u][k], s);
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
-                        acc[mt][nt] = mx4_mfma(it.x[mt][u].v[k], w, acc[mt][nt]);
-                }
-            }
-    } else {
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    __builtin_amdgcn_sched_barrier(0);       // one split at a time: registers
-                    bf16x8 hi, lo;
-                    split_f16(it.x[mt][u].v[k], hi, lo);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const bf16x8 w = mx4_to_bf16(it.w[nt][u][k], mx4_scale(it.ws[nt][u]));
-                        acc[mt][nt] = mx4_mfma(hi, w, acc[mt][nt]);
-                        acc[mt][nt] = mx4_mfma(lo, w, acc[mt][nt]);
-                    }
-                }
     }
 }
 
@@ -264,6 +293,153 @@ __device__ __forceinline__ void mx4_wave(const Mx4Rows<TX, MT, NT> &rows, f32x4 
             }
         }
     }
+}
+
+// ---------------------------------------------------------------------------
+// The streaming form, for few tokens: the activations of a stretch of columns
+// lie in LDS and every wave runs its own stream of weights through registers.
+// An item is 512 columns of 16 NT rows: four 16-byte loads of codes and one of
+// scales a lane and row tile.
+constexpr int kStreamBlocks = 16;              // blocks of 32 columns in an item
+
+template <int NT> struct StreamItem {
+    u32x4 w[NT][4], s[NT];
+};
+
+// A wave's 16 NT rows: scalar bases of the row tiles and one offset a lane (in
+// is at most 2^28 columns: 16 rows stay below 2^32 bytes).
+template <int NT> struct StreamRows {
+    const uint8_t *w[NT], *s[NT];
+    uint32_t wo, so;
+    // row r of the tile (or any other row of it), lane quarter c
+    __device__ __forceinline__ void lane(uint32_t row, int c, int nb)
+    {
+        so = row * (uint32_t)nb;
+        wo = so * 16 + c * 16;
+    }
+};
+
+// Words u of the item that begins at block b0; blocks past the rows' end load
+// the last one.
+template <int NT>
+__device__ __forceinline__ void stream_load_w(u32x4 (&w)[NT][4], int u, const StreamRows<NT> &rows, int b0, int nb,
+                                              int c)
+{
+    const int b4 = b0 + 4 * u, back = b4 + c < nb ? 0 : b4 + c - (nb - 1);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const uint8_t *const p = rows.w[nt] + (int64_t)b4 * 16;
+        if (b4 + 4 <= nb)
+            w[nt][u] = *reinterpret_cast<const u32x4 *>(p + rows.wo);
+        else
+            w[nt][u] = *reinterpret_cast<const u32x4 *>(p - back * 16 + (int64_t)rows.wo);
+    }
+}
+
+template <int NT>
+__device__ __forceinline__ void stream_load_s(u32x4 (&s)[NT], const StreamRows<NT> &rows, int b0, int nb)
+{
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+        if (b0 + kStreamBlocks <= nb)
+            __builtin_memcpy(&s[nt], rows.s[nt] + b0 + rows.so, 16);
+        else
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                s[nt][u] = mx4_scales4(rows.s[nt] + rows.so, b0 + 4 * u, nb);
+}
+
+template <int NT>
+__device__ __forceinline__ void stream_load(StreamItem<NT> &it, const StreamRows<NT> &rows, int b0, int nb, int c)
+{
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+        stream_load_w(it.w, u, rows, b0, nb, c);
+    stream_load_s(it.s, rows, b0, nb);
+}
+
+// acc += the item's products; x[mt] is the lane's activation row in LDS at the
+// item's first column, plus 8 c columns. `blocks` of the item exist; `tiles`:
+// which token tiles to multiply (bits). ROLL: the item of `next` at block
+// next_b0 takes its place, load by load as registers are used up (next_b0 < 0:
+// none). One register set then keeps a wave's stream going; with two row tiles
+// a wave, where registers allow it, two sets that change places are faster.
+template <bool WIDE, bool ROLL, typename TX, int MT, int NT>
+__device__ __forceinline__ void stream_compute(StreamItem<NT> &it, const TX *const (&x)[MT], f32x4 (&acc)[MT][NT],
+                                               int blocks, int tiles, const StreamRows<NT> &next, int next_b0, int nb,
+                                               int c, bool &bad)
+{
+    typedef typename Vec8<TX>::type vec;
+    u32x4 sn[NT];
+    if (ROLL && next_b0 >= 0)
+        stream_load_s(sn, next, next_b0, nb);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        __builtin_amdgcn_sched_barrier(0);             // one step's activations in registers at a time
+        u32x4 wu[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            wu[nt] = it.w[nt][u];
+            transpose4(wu[nt]);
+        }
+        if (ROLL && next_b0 >= 0)
+            stream_load_w(it.w, u, next, next_b0, nb, c);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            if (4 * u + s >= blocks)
+                break;
+            vec w[NT];
+            bf16x8 wide[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const uint32_t byte = it.s[nt][u] >> (8 * s) & 0xFFu;
+                if constexpr (WIDE) {
+                    wide[nt] = mx4_to_bf16(wu[nt][s], mx4_scale(byte));
+                } else if constexpr (std::is_same<TX, f16>::value) {
+                    w[nt] = mx4_to_f16(wu[nt][s], mx4_scale(byte));
+                    bad = bad || !mx4_fits_f16(byte);
+                } else {
+                    w[nt] = mx4_to_bf16(wu[nt][s], mx4_scale(byte));
+                }
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                if (MT > 1 && !(tiles >> mt & 1))
+                    continue;
+                const vec xv = load8(x[mt] + (4 * u + s) * 32);
+                if constexpr (WIDE) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    bf16x8 hi, lo;
+                    split_f16(xv, hi, lo);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        acc[mt][nt] = mx4_mfma(hi, wide[nt], acc[mt][nt]);
+                        acc[mt][nt] = mx4_mfma(lo, wide[nt], acc[mt][nt]);
+                    }
+                } else {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        acc[mt][nt] = mx4_mfma(xv, w[nt], acc[mt][nt]);
+                }
+            }
+        }
+    }
+    if (ROLL && next_b0 >= 0)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+            it.s[nt] = sn[nt];
+}
+
+// LDS for activations: rows of kc blocks, padded by 16 bytes (the eight rows
+// that one 128-byte LDS cycle serves then lie on distinct banks), kStreamLds
+// bytes without the padding. kc for `rows` rows (64 at most): a whole number
+// of items, all columns at most.
+constexpr int kStreamLds = 64 * 1024;
+__host__ __device__ inline int stream_chunk(int rows, int nb)
+{
+    const int fit = kStreamLds / (rows * 64 * kStreamBlocks) * kStreamBlocks;
+    const int all = (nb + kStreamBlocks - 1) / kStreamBlocks * kStreamBlocks;
+    return fit < all ? fit : all;
 }
 
 }  // namespace awq

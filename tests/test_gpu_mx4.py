@@ -412,7 +412,7 @@ def test_moe_refuses_a_short_workspace(awq):
     X, X32, R, R32, gu, dn = moe_inputs(4, 3, 64, 64, "bf16", 2)
     gc, gs, gcd, gsd = mx4(awq, gu)
     dc, ds, dcd, dsd = mx4(awq, dn)
-    n = awq.mx4_moe_workspace_size(4, 64, 2)
+    n = awq.mx4_moe_workspace_size(4, 64, 64, 2)
     with pytest.raises(ValueError):
         awq.mx4_moe(X, R, gcd, gsd, dcd, dsd, 2, workspace=torch.empty(n - 1, dtype=torch.uint8, device="cuda"))
     with pytest.raises(awq.AwqError):

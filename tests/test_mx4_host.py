@@ -97,10 +97,14 @@ def test_moe_refusals(L, kw, status):
 
 
 def test_moe_workspace_size(L):
-    n = awq.mx4_moe_workspace_size(4, 96, 2)
+    n = awq.mx4_moe_workspace_size(4, 4096, 96, 2)
     need = 8 * 4 + 8 * 4 + 8 * 96 * 2                  # ids, weights, intermediate
-    assert need <= n < need + 3 * 256
-    for bad in ((0, 96, 2), (65, 96, 2), (4, 0, 2), (4, 90, 2), (4, 96, 0), (4, 96, 17)):
+    need += 4 * 256 * 4                                # logits of up to 256 experts
+    assert need <= n < need + 4 * 256
+    # few hidden columns: the down product in parts, with fp32 sums of each
+    assert awq.mx4_moe_workspace_size(33, 1056, 1408, 4) >= 33 * 4 * (8 + 1408 * 2) + 33 * 1024 + 3 * 33 * 1056 * 4
+    for bad in ((0, 64, 96, 2), (65, 64, 96, 2), (4, 0, 96, 2), (4, 40, 96, 2), (4, 64, 0, 2), (4, 64, 90, 2),
+                (4, 64, 96, 0), (4, 64, 96, 17)):
         assert awq.mx4_moe_workspace_size(*bad) == 0
 
 
