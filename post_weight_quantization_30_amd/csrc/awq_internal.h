@@ -306,10 +306,11 @@ hipError_t launch_mx4_gemm_a4(const uint8_t *xcodes, const uint8_t *xscales, int
                               hipStream_t st);
 // Parts that the down product's contraction is shared out to: with fewer than
 // 256 tiles of 16 hidden columns as many as keep every unit busy, but no part
-// without 16 waves' worth of 512-column units (`routed`: experts at most).
-inline int mx4_moe_parts(int64_t hidden, int64_t inter, int64_t routed)
+// without 16 waves' worth of 512-column units (`groups`: of one
+// expert's 16 tokens at most, as many as there can be).
+inline int mx4_moe_parts(int64_t hidden, int64_t inter, int64_t groups)
 {
-    const int64_t fill = 256 / (hidden / 16), work = routed * ((inter + 511) / 512) / 32;
+    const int64_t fill = 256 / (hidden / 16), work = groups * ((inter + 511) / 512) / 32;
     const int64_t z = fill < work ? fill : work;
     return (int)(z < 1 ? 1 : z > 8 ? 8 : z);
 }
@@ -323,7 +324,7 @@ inline Mx4MoeWs mx4_moe_ws_layout(int64_t M, int64_t hidden, int64_t inter, int 
 {
     Mx4MoeWs w;
     const size_t pairs = (size_t)(M * top_k);
-    const int parts = mx4_moe_parts(hidden, inter, M * top_k);      // at least those of any number of experts
+    const int parts = mx4_moe_parts(hidden, inter, M * top_k + M * top_k / 16);    // any number of experts
     w.ids_off = 0;
     w.w_off = align256(pairs * sizeof(int32_t));
     w.h_off = w.w_off + align256(pairs * sizeof(float));

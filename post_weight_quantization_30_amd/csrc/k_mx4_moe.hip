@@ -141,15 +141,23 @@ __global__ __launch_bounds__(64) void k_mx4_moe_topk(const float *__restrict__ l
     }
 }
 
-// What a block of `up` or `down` makes of the routing's ids: of every expert the
-// tokens (bits) and where its pairs begin in the list of pairs by expert and
-// token; the routed experts in ascending order.
+// What a block of `up` or `down` makes of the routing's ids: the (token, slot)
+// pairs by expert and token, cut into groups of one expert's 16 at most.
+constexpr int kMaxPairs = kMaxTok * kMaxK, kMaxGroups = kMaxE + kMaxPairs / 16;
+
 struct Routed {
-    uint64_t tokens[kMaxE];
+    uint64_t tokens[kMaxE];                            // of every expert, as bits
     uint32_t sums[kMaxE / 64];
-    uint16_t first[kMaxE], pairs[kMaxTok * kMaxK];
-    uint8_t expert[kMaxE], of_pair[kMaxTok * kMaxK];
-    int active;
+    uint16_t first[kMaxE];                             // an expert's first place in `pairs`
+    uint16_t pairs[kMaxPairs], group_of[kMaxPairs];    // group_of: by place
+    uint16_t begin[kMaxGroups + 1];                    // a group's first place; begin[groups] = all pairs
+    uint8_t expert[kMaxGroups];
+    int groups;
+    // uniform: a group's size
+    __device__ __forceinline__ int size(int g) const
+    {
+        return __builtin_amdgcn_readfirstlane(begin[g + 1] - begin[g]);
+    }
 };
 
 __device__ __forceinline__ void read_routing(Routed &rt, const int32_t *ids, int pairs, int top_k)
@@ -161,11 +169,11 @@ __device__ __forceinline__ void read_routing(Routed &rt, const int32_t *ids, int
     for (int p = t; p < pairs; p += blockDim.x)
         atomicOr((unsigned long long *)&rt.tokens[ids[p]], 1ull << (p / top_k));   // any order gives the same bits
     __syncthreads();
-    // prefix sums over the experts, one a thread: pairs below 65536, experts above
+    // prefix sums over the experts, one a thread: pairs below 65536, groups above
     uint32_t own = 0, sum = 0;
     if (t < kMaxE) {
-        const int n = __popcll(rt.tokens[t]);
-        own = sum = n ? 0x10000u + n : 0;
+        const uint32_t n = __popcll(rt.tokens[t]);
+        own = sum = (n + 15) / 16 << 16 | n;
         for (int off = 1; off < 64; off <<= 1) {
             const uint32_t o = __shfl_up(sum, off);
             sum += lane >= off ? o : 0;
@@ -177,27 +185,33 @@ __device__ __forceinline__ void read_routing(Routed &rt, const int32_t *ids, int
     if (t < kMaxE) {
         for (int q = 0; q < t >> 6; ++q)
             sum += rt.sums[q];
-        rt.first[t] = (uint16_t)(sum - own);
-        if (own)
-            rt.expert[(sum - own) >> 16] = (uint8_t)t;
-        if (t == kMaxE - 1)
-            rt.active = (int)(sum >> 16);
+        const uint32_t before = sum - own;
+        rt.first[t] = (uint16_t)before;
+        for (uint32_t k = 0; k < own >> 16; ++k) {
+            rt.expert[(before >> 16) + k] = (uint8_t)t;
+            rt.begin[(before >> 16) + k] = (uint16_t)(before + 16 * k);
+        }
+        if (t == kMaxE - 1) {
+            rt.groups = (int)(sum >> 16);
+            rt.begin[sum >> 16] = (uint16_t)sum;
+        }
     }
     __syncthreads();
     for (int p = t; p < pairs; p += blockDim.x) {
-        const int e = ids[p];
-        const int at = rt.first[e] + __popcll(rt.tokens[e] & ((1ull << (p / top_k)) - 1));
-        rt.pairs[at] = (uint16_t)p;
-        rt.of_pair[at] = (uint8_t)e;
+        const int e = ids[p], nth = (int)__popcll(rt.tokens[e] & ((1ull << (p / top_k)) - 1));
+        rt.pairs[rt.first[e] + nth] = (uint16_t)p;
     }
+    for (int g = t; g < rt.groups; g += blockDim.x)
+        for (int k = rt.begin[g]; k < rt.begin[g + 1]; ++k)
+            rt.group_of[k] = (uint16_t)g;
     __syncthreads();
 }
 
 // ---- gate and up ------------------------------------------------------------
-// Block: 8 / S tiles of 16 columns of one expert's intermediate (16 gate rows
-// and 16 up rows each), blockIdx.z's sixteen of the tokens routed to the expert,
-// S waves a tile splitting the hidden columns. The tokens' activations lie in
-// LDS by chunks of kc blocks; every wave streams its weights (see StreamItem).
+// Block: a group's tokens, 8 / S tiles of 16 columns of its expert's
+// intermediate (16 gate rows and 16 up rows each), S waves a tile splitting the
+// hidden columns. The tokens' activations lie in LDS by chunks of kc blocks;
+// every wave streams its weights (see StreamItem).
 constexpr int kUpWaves = 8;
 
 template <typename TX, int S>
@@ -213,12 +227,10 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void k_mx4_moe_up(const TX *__res
     __shared__ __align__(16) uint8_t lds[kStreamLds + 16 * 16];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     read_routing(rt, ids, pairs, top_k);
-    if ((int)blockIdx.y >= rt.active)
-        return;                    // fewer routed experts than blocks: the whole block leaves
-    const int e = __builtin_amdgcn_readfirstlane(rt.expert[blockIdx.y]);
-    const int all = (int)__popcll(rt.tokens[e]), t0 = (int)blockIdx.z * 16;
-    if (t0 >= all)
-        return;
+    const int group = (int)blockIdx.y;
+    if (group >= rt.groups)
+        return;                    // fewer groups than blocks: the whole block leaves
+    const int e = __builtin_amdgcn_readfirstlane(rt.expert[group]);
     const int nb = hidden / kMxBlock, r = lane & 15, c = lane >> 4, part = wave % S;
     const int col0 = ((int)blockIdx.x * (kUpWaves / S) + wave / S) * 16;
     const int64_t row = (int64_t)e * 2 * inter + (col0 < inter ? col0 : 0);          // past the end: not stored
@@ -227,8 +239,8 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void k_mx4_moe_up(const TX *__res
     rows.lane(r, c, nb);
     const int items = (nb + kStreamBlocks - 1) / kStreamBlocks;
 
-    const uint16_t *const list = rt.pairs + rt.first[e] + t0;
-    const int count = __builtin_amdgcn_readfirstlane(all - t0 < 16 ? all - t0 : 16);
+    const uint16_t *const list = rt.pairs + rt.begin[group];
+    const int count = rt.size(group);
     const int kc = stream_chunk(count, nb), stride = kc * 64 + 16, per = kc / kStreamBlocks;
     const int xrow = (r < count ? r : count - 1) * stride + c * 16;
     bool bad = false;
@@ -303,115 +315,104 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void k_mx4_moe_up(const TX *__res
 }
 
 // ---- down -------------------------------------------------------------------
-// Block: 16 hidden columns, all tokens, 16 waves (8 for more than 16 tokens:
-// registers). The contraction is a list of units, 512 columns of one routed
-// expert each, by expert and column. A unit's activations are one row of 1 KB
-// for each token that the expert serves; a stage is as many units as have 64
-// rows at most, in one of two LDS buffers, and the waves take its units in turn.
-// A stage's rows are on their way to registers while the one before it is
-// multiplied, and so are every wave's next weights, across the stages'
-// barriers. A token that an expert does not serve multiplies some other row
-// and drops the result: an expert's NaN reaches its own tokens only. With few
-// hidden columns the units are shared out over gridDim.y blocks, whose fp32
+// Block: 16 hidden columns, all tokens, 16 waves. The contraction is a list of
+// units, 512 columns of one group's expert each, by group and column. A unit's
+// activations are one row of 1 KB for each of the group's tokens; a stage is as
+// many units as have ROWS rows at most, in one of two LDS buffers, and the
+// waves take its units in turn. A stage's rows are on their way to registers
+// while the one before it is multiplied, and so are every wave's next weights,
+// across the stages' barriers. A unit's results, one row for each of its
+// tokens, go to the wave's own sums of all tokens in LDS: an expert's NaN
+// reaches its own tokens only, and the order of all additions is fixed. With
+// few hidden columns the units are shared out over gridDim.y blocks, whose fp32
 // sums k_mx4_moe_sum adds (`sums`: (gridDim.y, M, hidden)).
 constexpr int kRowBytes = 64 * kStreamBlocks + 16;     // of a row in LDS, padded (see stream_chunk)
-constexpr int kDownRows = 64;                          // of a stage
-template <int MT> constexpr int kDownWavesOf = MT == 1 ? 16 : 8;
+constexpr int kDownWaves = 16;
 
-template <typename TX, int MT>
-__global__ __launch_bounds__(64 * kDownWavesOf<MT>) void k_mx4_moe_down(const TX *__restrict__ h, int M, int hidden, int inter,
+template <typename TX, int TOK, int ROWS>
+__global__ __launch_bounds__(64 * kDownWaves) void k_mx4_moe_down(const TX *__restrict__ h, int M, int hidden, int inter,
                                                                   int top_k, const int32_t *__restrict__ ids,
                                                                   const uint8_t *__restrict__ codes,
                                                                   const uint8_t *__restrict__ scales,
                                                                   TX *__restrict__ Y, float *__restrict__ sums)
 {
-    constexpr int kWaves = kDownWavesOf<MT>;
-    constexpr int kRegs = kDownRows / kWaves;          // rows a wave moves in a stage
-    __shared__ __align__(16) uint8_t bufs[2][kDownRows * kRowBytes];
+    constexpr int kRegs = (ROWS + kDownWaves - 1) / kDownWaves;    // rows a wave moves in a stage
+    __shared__ __align__(16) uint8_t bufs[2][ROWS * kRowBytes];
+    __shared__ float out[kDownWaves][TOK * 16];
     __shared__ Routed rt;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, c = lane >> 4;
     read_routing(rt, ids, M * top_k, top_k);
-    const int active = __builtin_amdgcn_readfirstlane(rt.active);
-    const int nb = inter / kMxBlock, per = (nb + kStreamBlocks - 1) / kStreamBlocks;   // units of an expert
+    const int groups = __builtin_amdgcn_readfirstlane(rt.groups);
+    const int nb = inter / kMxBlock, per = (nb + kStreamBlocks - 1) / kStreamBlocks;   // units of a group
 
-    // Rows in unit order: expert e's begin at per * first[e], unit i's at
-    // + i * count. A stage: units u0 ... u0 + units - 1, rows r0 ... r0 + rows - 1.
+    // Rows in unit order: group g's begin at per * begin[g], unit i's at + i *
+    // size. A stage: units u0 ... u0 + units - 1, rows r0 ... r0 + rows - 1.
     struct Stage {                                     // uniform
         int u0, units, r0, rows;
     };
-    const int first_unit = (int)((int64_t)per * active * blockIdx.y / gridDim.y);
-    const int end_unit = (int)((int64_t)per * active * (blockIdx.y + 1) / gridDim.y);
+    const int first_unit = (int)((int64_t)per * groups * blockIdx.y / gridDim.y);
+    const int end_unit = (int)((int64_t)per * groups * (blockIdx.y + 1) / gridDim.y);
     auto open = [&](Stage &s, int u0) {
         s.u0 = u0;
         s.units = s.rows = s.r0 = 0;
         if (u0 >= end_unit)
             return;
-        const int rank = u0 / per, i = u0 - rank * per;
-        const int e = rt.expert[rank];
-        const int count = __builtin_amdgcn_readfirstlane(__popcll(rt.tokens[e]));
-        s.r0 = __builtin_amdgcn_readfirstlane(per * rt.first[e]) + i * count;
-        const int left = per - i, fit = kDownRows / count;
-        if (fit < left) {                              // ends inside this expert
+        const int g = u0 / per, i = u0 - g * per, count = rt.size(g);
+        s.r0 = per * __builtin_amdgcn_readfirstlane(rt.begin[g]) + i * count;
+        const int left = per - i, fit = ROWS / count;
+        if (fit < left) {                              // ends inside this group
             s.units = fit < end_unit - u0 ? fit : end_unit - u0;
             s.rows = s.units * count;
             return;
         }
-        // lane l: whether the stage holds all of the experts up to rank + l
-        const int k = rank + lane < active ? rt.expert[rank + lane] : e;
-        const int end = per * (rt.first[k] + (int)__popcll(rt.tokens[k])) - s.r0;
-        const uint64_t whole = __ballot(rank + lane < active && end <= kDownRows);
-        const int n = __popcll(whole);                 // a run from lane 0 on: ends only grow
-        const int used = __builtin_amdgcn_readfirstlane(__shfl(end, n - 1));
+        // lane l: whether the stage holds all of the groups up to g + l
+        const int end = per * rt.begin[g + lane < groups ? g + lane + 1 : groups] - s.r0;
+        const int n = (int)__popcll(__ballot(g + lane < groups && end <= ROWS));   // a run from lane 0 on: ends grow
+        s.rows = __builtin_amdgcn_readfirstlane(__shfl(end, n - 1));
         s.units = left + (n - 1) * per;
-        s.rows = used;
-        if (rank + n < active) {                       // and some units of the next
-            const int cnt = __builtin_amdgcn_readfirstlane(__popcll(rt.tokens[rt.expert[rank + n]]));
-            const int more = (kDownRows - used) / cnt;
+        if (g + n < groups) {                          // and some units of the next
+            const int size = rt.size(g + n), more = (ROWS - s.rows) / size;
             s.units += more < per ? more : per - 1;
-            s.rows += (more < per ? more : per - 1) * cnt;
+            s.rows += (more < per ? more : per - 1) * size;
         }
         if (s.units > end_unit - u0)                   // the rows past the last unit are moved, not used
             s.units = end_unit - u0;
     };
     u32x4 pre[kRegs];
-    auto row_source = [&](const Stage &s, int q, int &chunks) -> const TX * {
-        const int R = s.r0 + wave + q * kWaves, at = R / per;      // `at` lies in the expert's pairs
-        const int e = rt.of_pair[at], first = rt.first[e], count = (int)__popcll(rt.tokens[e]);
-        const int local = R - per * first, i = local / count, p = rt.pairs[first + local - i * count];
-        chunks = (nb - i * kStreamBlocks < kStreamBlocks ? nb - i * kStreamBlocks : kStreamBlocks) * 4;
-        return h + ((int64_t)p * nb + i * kStreamBlocks) * 32;
-    };
     auto fetch = [&](const Stage &s) {
 #pragma unroll
         for (int q = 0; q < kRegs; ++q)
-            if (wave + q * kWaves < s.rows) {
-                int chunks;
-                const TX *const src = row_source(s, q, chunks);
-                if (lane < chunks)
-                    pre[q] = *reinterpret_cast<const u32x4 *>(src + lane * 8);
+            if (wave + q * kDownWaves < s.rows) {
+                const int R = s.r0 + wave + q * kDownWaves, at = R / per;      // `at` lies among the group's pairs
+                const int g = __builtin_amdgcn_readfirstlane(rt.group_of[at]), size = rt.size(g);
+                const int begin = __builtin_amdgcn_readfirstlane(rt.begin[g]);
+                const int local = R - per * begin, i = local / size;
+                const int p = __builtin_amdgcn_readfirstlane(rt.pairs[begin + local - i * size]);
+                if (lane < (nb - i * kStreamBlocks) * 4)
+                    pre[q] = *reinterpret_cast<const u32x4 *>(h + ((int64_t)p * nb + i * kStreamBlocks) * 32 + lane * 8);
             }
     };
     auto stash = [&](const Stage &s, uint8_t *buf) {   // lanes past a row's end store what nothing reads
 #pragma unroll
         for (int q = 0; q < kRegs; ++q)
-            if (wave + q * kWaves < s.rows)
-                *reinterpret_cast<u32x4 *>(buf + (wave + q * kWaves) * kRowBytes + lane * 16) = pre[q];
+            if (wave + q * kDownWaves < s.rows)
+                *reinterpret_cast<u32x4 *>(buf + (wave + q * kDownWaves) * kRowBytes + lane * 16) = pre[q];
     };
     StreamRows<1> rows;
     rows.lane(r, c, nb);
     auto aim = [&](int u) -> int {                     // rows of the unit's expert; the unit's first block
-        const int rank = u / per;
-        const int64_t row = (int64_t)__builtin_amdgcn_readfirstlane(rt.expert[rank]) * hidden + blockIdx.x * 16;
+        const int g = u / per;
+        const int64_t row = (int64_t)__builtin_amdgcn_readfirstlane(rt.expert[g]) * hidden + blockIdx.x * 16;
         rows.w[0] = codes + row * nb * 16;
         rows.s[0] = scales + row * nb;
-        return (u - rank * per) * kStreamBlocks;
+        return (u - g * per) * kStreamBlocks;
     };
     bool bad = false;
-    f32x4 acc[MT][1];
 
     auto contract = [&]<bool WIDE>() {
-        mx4_zero(acc);
+        for (int k = lane; k < TOK * 16; k += 64)
+            out[wave][k] = 0.f;
         Stage cur, nxt;
         open(cur, first_unit);
         fetch(cur);
@@ -427,32 +428,27 @@ __global__ __launch_bounds__(64 * kDownWavesOf<MT>) void k_mx4_moe_down(const TX
 #pragma unroll 1
         while (cur.units) {
 #pragma unroll 1
-            for (int j = wave; j < cur.units; j += kWaves) {
-                const int u = cur.u0 + j, rank = u / per, i = u - rank * per;
-                const int e = __builtin_amdgcn_readfirstlane(rt.expert[rank]);
-                const uint64_t set = rt.tokens[e];
-                const int count = (int)__popcll(set), row0 = per * rt.first[e] + i * count - cur.r0;
-                const TX *x[MT];
-                int tiles = 0;
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    const int tok = 16 * mt + r, pos = (int)__popcll(set & ((1ull << tok) - 1));
-                    x[mt] = (const TX *)(now + (row0 + (pos < count ? pos : count - 1)) * kRowBytes + c * 16);
-                    tiles |= (set >> (16 * mt) & 0xFFFF ? 1 : 0) << mt;
-                }
-                tiles = __builtin_amdgcn_readfirstlane(tiles);
-                const int ahead = j + kWaves < cur.units ? cur.u0 + j + kWaves : wave < nxt.units ? nxt.u0 + wave : -1;
+            for (int j = wave; j < cur.units; j += kDownWaves) {
+                const int u = cur.u0 + j, g = u / per, i = u - g * per;
+                const int count = rt.size(g), begin = __builtin_amdgcn_readfirstlane(rt.begin[g]);
+                const int row0 = per * begin + i * count - cur.r0;
+                const TX *const x[1] = {
+                    (const TX *)(now + (row0 + (r < count ? r : count - 1)) * kRowBytes + c * 16)};
+                const int ahead =
+                    j + kDownWaves < cur.units ? cur.u0 + j + kDownWaves : wave < nxt.units ? nxt.u0 + wave : -1;
                 loaded = ahead >= 0;
                 const int next_b0 = loaded ? aim(ahead) : -1;
-                const TX *const(&xr)[MT] = x;
-                f32x4 part[MT][1];
+                f32x4 part[1][1];
                 mx4_zero(part);
-                stream_compute<WIDE, true>(it, xr, part, nb - i * kStreamBlocks, tiles, rows, next_b0, nb, c, bad);
+                stream_compute<WIDE, true>(it, x, part, nb - i * kStreamBlocks, 1, rows, next_b0, nb, c, bad);
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        acc[mt][0][k] += set >> (16 * mt + 4 * c + k) & 1 ? part[mt][0][k] : 0.0f;
+                for (int k = 0; k < 4; ++k)
+                    if (4 * c + k < count) {
+                        const int tok = rt.pairs[begin + 4 * c + k] / top_k;
+                        out[wave][tok * 16 + r] += part[0][0][k];
+                    }
+                // another lane may add to the same place next time
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             }
             if (!loaded && wave < nxt.units) {         // nothing was left for it in this stage
                 loaded = true;
@@ -473,26 +469,17 @@ __global__ __launch_bounds__(64 * kDownWavesOf<MT>) void k_mx4_moe_down(const TX
         if (__syncthreads_or(bad))                     // scales that fp16 cannot hold
             contract.template operator()<true>();
 
-    f32x4 *const red = reinterpret_cast<f32x4 *>(bufs[0]);
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-        red[(wave * MT + mt) * 64 + lane] = acc[mt][0];
     __syncthreads();
-    for (int idx = threadIdx.x; idx < MT * 64; idx += 64 * kWaves) {
-        f32x4 sum = red[idx];
+    for (int k = threadIdx.x; k < M * 16; k += 64 * kDownWaves) {
+        float sum = out[0][k];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w)
-            sum += red[w * MT * 64 + idx];
-        const int l = idx & 63, m = 16 * (idx / 64) + 4 * (l >> 4);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (m + k < M) {
-                const int64_t at = (int64_t)(m + k) * hidden + blockIdx.x * 16 + (l & 15);
-                if (gridDim.y > 1)
-                    sums[blockIdx.y * (int64_t)M * hidden + at] = sum[k];
-                else
-                    Y[at] = static_cast<TX>(sum[k]);
-            }
+        for (int w = 1; w < kDownWaves; ++w)
+            sum += out[w][k];
+        const int64_t at = (int64_t)(k >> 4) * hidden + blockIdx.x * 16 + (k & 15);
+        if (gridDim.y > 1)
+            sums[blockIdx.y * (int64_t)M * hidden + at] = sum;
+        else
+            Y[at] = static_cast<TX>(sum);
     }
 }
 
@@ -520,16 +507,16 @@ void up(const TX *X, int pairs, int most, int hidden, int inter, int top_k, cons
         const uint8_t *gu, const uint8_t *gus, TX *h, hipStream_t st)
 {
     const int tiles = inter / 16, per = kUpWaves / S;
-    k_mx4_moe_up<TX, S><<<dim3((tiles + per - 1) / per, most, (pairs / top_k + 15) / 16), 64 * kUpWaves, 0, st>>>(
-        X, pairs, hidden, inter, top_k, ids, weights, gu, gus, h);
+    k_mx4_moe_up<TX, S><<<dim3((tiles + per - 1) / per, most), 64 * kUpWaves, 0, st>>>(X, pairs, hidden, inter, top_k,
+                                                                                      ids, weights, gu, gus, h);
 }
 
-template <typename TX, int MT>
+template <typename TX, int TOK, int ROWS>
 void down(int Z, const TX *h, int M, int hidden, int inter, int top_k, const int32_t *ids, const uint8_t *dn,
           const uint8_t *dns, TX *Y, float *sums, hipStream_t st)
 {
-    k_mx4_moe_down<TX, MT><<<dim3(hidden / 16, Z), 64 * kDownWavesOf<MT>, 0, st>>>(h, M, hidden, inter, top_k, ids, dn,
-                                                                                  dns, Y, sums);
+    k_mx4_moe_down<TX, TOK, ROWS><<<dim3(hidden / 16, Z), 64 * kDownWaves, 0, st>>>(h, M, hidden, inter, top_k, ids,
+                                                                                   dn, dns, Y, sums);
 }
 
 template <typename TX>
@@ -543,7 +530,7 @@ hipError_t moe(const void *X, int M, int hidden, int inter, int E, int top_k, in
     float *const sums = (float *)(ws + lay.sums_off);
     TX *const h = (TX *)(ws + lay.h_off);
     const TX *const x = (const TX *)X, *const rw = (const TX *)router;
-    const int pairs = M * top_k, most = pairs < E ? pairs : E;     // routed experts at most
+    const int pairs = M * top_k, most = (pairs < E ? pairs : E) + (M > 16 ? pairs / 16 : 0);   // groups at most
     if (M == 1)
         logits<TX, 1>(x, M, hidden, rw, E, lg, st);
     else if (M <= 4)
@@ -563,11 +550,9 @@ hipError_t moe(const void *X, int M, int hidden, int inter, int E, int top_k, in
         up<TX, 8>(x, pairs, most, hidden, inter, top_k, ids, weights, gu, gus, h, st);
     const int Z = mx4_moe_parts(hidden, inter, most);
     if (M <= 16)
-        down<TX, 1>(Z, h, M, hidden, inter, top_k, ids, dn, dns, (TX *)Y, sums, st);
-    else if (M <= 32)
-        down<TX, 2>(Z, h, M, hidden, inter, top_k, ids, dn, dns, (TX *)Y, sums, st);
+        down<TX, 16, 64>(Z, h, M, hidden, inter, top_k, ids, dn, dns, (TX *)Y, sums, st);
     else
-        down<TX, 4>(Z, h, M, hidden, inter, top_k, ids, dn, dns, (TX *)Y, sums, st);
+        down<TX, kMaxTok, 40>(Z, h, M, hidden, inter, top_k, ids, dn, dns, (TX *)Y, sums, st);
     if (Z > 1)
         k_mx4_moe_sum<TX><<<dim3((M * hidden + 255) / 256), 256, 0, st>>>(sums, M * hidden, Z, (TX *)Y);
     return hipGetLastError();
