@@ -460,7 +460,7 @@ int mx4_shape(int64_t rows, int64_t in)
 {
     if (rows < 1 || in < 1 || in % AWQ_MX4_BLOCK != 0 || rows > INT64_MAX / in)
         return AWQ_ERR_INVALID_ARG;
-    if (rows * in > (int64_t)1 << 43 || in > (int64_t)1 << 28)
+    if (rows * in > (int64_t)1 << 43 || in > (int64_t)1 << 23)
         return AWQ_ERR_UNSUPPORTED;
     return AWQ_OK;
 }
@@ -470,7 +470,7 @@ int mx4_gemm_shape(int64_t M, int64_t in, int64_t out)
     if (M < 1 || out < 1 || in < 1 || in % AWQ_MX4_BLOCK != 0 || out > INT64_MAX / in || M > INT64_MAX / in ||
         M > INT64_MAX / out)
         return AWQ_ERR_INVALID_ARG;
-    if (M > 65535LL * 32 || in > (int64_t)1 << 28 || (out + 15) / 16 > (int64_t)0x7fffffff)
+    if (M > 65535LL * 32 || in > (int64_t)1 << 23 || (out + 15) / 16 > (int64_t)0x7fffffff)
         return AWQ_ERR_UNSUPPORTED;
     return AWQ_OK;
 }

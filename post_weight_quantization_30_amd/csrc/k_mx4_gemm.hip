@@ -227,9 +227,6 @@ __device__ __forceinline__ void store_tiles(TY *__restrict__ Y, const f32x16 (&a
         }
 }
 
-// Columns up to which the tile kernels' 32-bit offsets within a tile hold.
-constexpr int64_t kTileMaxIn = (int64_t)1 << 21;
-
 // 16-bit activations. Block: 128 tokens x 256 rows, 4 waves of 128 x 64. A
 // step is 64 columns: 128 bytes of every activation row go to LDS as eight
 // 16-byte chunks, chunk q of row m at position q ^ (m & 7), so that the eight
@@ -263,7 +260,8 @@ __global__ __launch_bounds__(256, 2) void k_mx4_gemm_tile(const TX *__restrict__
     const int steps = (nb + 1) / 2, full = nb / 2;
 
     // Addresses are a scalar base (this tile, this step) and a 32-bit offset a
-    // lane. Rows past the ends load the last row: their results are not stored.
+    // lane (rows have at most 2^23 columns). Rows past the ends load the last
+    // row: their results are not stored.
     const uint8_t *const xbase = (const uint8_t *)X + m0 * xrow;
     const uint8_t *const wbase = codes + n0 * nb * 16, *const wsbase = scales + n0 * nb;
     const uint32_t mlast = (uint32_t)(M - 1 - m0 < BM - 1 ? M - 1 - m0 : BM - 1);
@@ -387,6 +385,152 @@ __global__ __launch_bounds__(256, 2) void k_mx4_gemm_tile(const TX *__restrict__
         if (__syncthreads_or(bad))
             contract.template operator()<true>();
     store_tiles<TY, MT, NT>(Y, acc, m0, n0 + 64 * wave, M, out, r, h);
+}
+
+// 16-bit activations, too few 128 x 256 tiles for the chip. Block: 32 MT tokens
+// x 64 rows, 8 waves: two of 32 rows each in four groups that take the steps of
+// 64 columns in turn, each with its own LDS buffers (laid out as above); the
+// groups' sums meet in LDS. 64 x 64 tiles keep all units busy from about 200
+// tokens x 4000 rows on, and a token's row is read in whole 128-byte lines
+// (read in matrix order, 64 bytes of 16 rows at a time, it kept the load units
+// busy for twice as long as everything else took).
+template <typename TX, typename TY, int MT>
+__global__ __launch_bounds__(512, 4) void k_mx4_gemm_mid(const TX *__restrict__ X, int64_t M, int nb,
+                                                         const uint8_t *__restrict__ codes,
+                                                         const uint8_t *__restrict__ scales, int64_t out,
+                                                         TY *__restrict__ Y)
+{
+    typedef typename Vec8<TX>::type vec;
+    constexpr int BM = 32 * MT, BN = 64, G = 4;
+    constexpr int CH = BM * 8 / 128;                   // activation chunks a thread moves in a step
+    __shared__ __align__(16) u32x4 lds[2][G][BM * 8];
+
+    int64_t m0, n0;
+    if (!tile_of_block((M + BM - 1) / BM, (out + BN - 1) / BN, m0, n0))
+        return;
+    m0 *= BM;
+    n0 *= BN;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 31, h = lane >> 5, group = wave >> 1, wn = wave & 1, gt = threadIdx.x & 127;
+    const int xrow = nb * 64;                          // bytes of an activation row
+    const int steps = (nb + 1) / 2, full = nb / 2;
+
+    const uint8_t *const xbase = (const uint8_t *)X + m0 * xrow;
+    const uint8_t *const wbase = codes + n0 * nb * 16, *const wsbase = scales + n0 * nb;
+    const uint32_t mlast = (uint32_t)(M - 1 - m0 < BM - 1 ? M - 1 - m0 : BM - 1);
+    const uint32_t nlast = (uint32_t)(out - 1 - n0 < BN - 1 ? out - 1 - n0 : BN - 1);
+    uint32_t xo[CH];
+    int xdst[CH];
+    const int xq = gt & 7;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        const uint32_t row = (gt + i * 128) >> 3;
+        xdst[i] = row * 8 + (xq ^ (row & 7));
+        xo[i] = (row < mlast ? row : mlast) * (uint32_t)xrow + xq * 16;
+    }
+    const uint32_t wr = 32 * wn + r, wrow = wr < nlast ? wr : nlast;
+    const uint32_t wo = wrow * (uint32_t)nb * 16 + h * 16, wso = wrow * (uint32_t)nb + h;
+
+    f32x16 acc[MT];
+    u32x4 xr[CH], w, wnext;
+    uint32_t ws, wsnext;
+    bool bad = false;
+
+    // steps past the last one are fetched as that one and dropped; for an odd
+    // last block see k_mx4_gemm_tile
+    auto fetch = [&](int k) {
+        k = k < steps ? k : steps - 1;
+        const bool end = k >= full;
+        const uint32_t xback = end && xq >= 4 ? 64 : 0, wback = end && h ? 1 : 0;
+        const uint8_t *const px = xbase + (int64_t)k * 128, *const pw = wbase + (int64_t)k * 32;
+        const uint8_t *const ps = wsbase + k * 2;
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+            xr[i] = *reinterpret_cast<const u32x4 *>(px + (xo[i] - xback));
+        wnext = *reinterpret_cast<const u32x4 *>(pw + (wo - 16 * wback));
+        wsnext = ps[wso - wback];
+    };
+    auto stash = [&](int k, int buf) {
+        if (k >= full && xq >= 4)
+#pragma unroll
+            for (int i = 0; i < CH; ++i)
+                xr[i] = u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+            lds[buf][group][xdst[i]] = xr[i];
+        w = wnext;
+        ws = k >= full && h ? 127 : wsnext;
+    };
+    auto contract = [&]<bool WIDE>() {
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+            acc[a] = f32x16{};
+        fetch(group);
+        stash(group, 0);
+        __syncthreads();
+        int buf = 0;
+        for (int k0 = 0; k0 < steps; k0 += G, buf ^= 1) {
+            const int k = k0 + group;
+            const bool more = k0 + G < steps;
+            if (more)
+                fetch(k + G);
+            if (k < steps) {
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    vec wv;
+                    bf16x8 wide;
+                    if constexpr (WIDE) {
+                        wide = mx4_to_bf16(w[s], mx4_scale(ws));
+                    } else if constexpr (std::is_same<TX, f16>::value) {
+                        wv = mx4_to_f16(w[s], mx4_scale(ws));
+                        bad = bad || !mx4_fits_f16(ws);
+                    } else {
+                        wv = mx4_to_bf16(w[s], mx4_scale(ws));
+                    }
+#pragma unroll
+                    for (int a = 0; a < MT; ++a) {
+                        const int row = 32 * a + r;
+                        const u32x4 x = lds[buf][group][row * 8 + ((4 * h + s) ^ (row & 7))];
+                        if constexpr (WIDE) {
+                            bf16x8 hi, lo;
+                            split_f16(__builtin_bit_cast(f16x8, x), hi, lo);
+                            acc[a] = mfma32(hi, wide, acc[a]);
+                            acc[a] = mfma32(lo, wide, acc[a]);
+                        } else {
+                            acc[a] = mfma32(__builtin_bit_cast(vec, x), wv, acc[a]);
+                        }
+                    }
+                }
+            }
+            if (more)
+                stash(k + G, buf ^ 1);
+            __syncthreads();
+        }
+    };
+    contract.template operator()<false>();
+    if constexpr (std::is_same<TX, f16>::value)
+        if (__syncthreads_or(bad))                     // scales that fp16 cannot hold
+            contract.template operator()<true>();
+
+    // the groups' sums, added in group order
+    float *const red = reinterpret_cast<float *>(lds);         // [G][BM][BN]
+#pragma unroll
+    for (int a = 0; a < MT; ++a)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            red[(group * BM + 32 * a + 8 * (i / 4) + 4 * h + i % 4) * BN + 32 * wn + r] = acc[a][i];
+    __syncthreads();
+    const int n = threadIdx.x & (BN - 1);
+#pragma unroll
+    for (int q = 0; q < BM / 8; ++q) {
+        const int m = (threadIdx.x >> 6) + 8 * q;
+        float sum = red[m * BN + n];
+#pragma unroll
+        for (int g = 1; g < G; ++g)
+            sum += red[(g * BM + m) * BN + n];
+        if (m0 + m < M && n0 + n < out)
+            Y[(m0 + m) * out + n0 + n] = static_cast<TY>(sum);
+    }
 }
 
 // MXFP4 activations. Block: 256 x 256, 4 waves of 128 x 128 (256 accumulator
@@ -554,19 +698,25 @@ hipError_t gemm(const void *X, const uint8_t *xs, int64_t M, int nb, const uint8
     if (M <= 16)
         return split<TX, TY, 1, 1, 4>(X, xs, M, nb, codes, scales, out, Y, st);
     if constexpr (std::is_same<TX, Mx4Act>::value) {
-        if (nb * 32 <= kTileMaxIn && tiles_of(M, 256) * tiles_of(out, 256) >= 64) {
+        if (tiles_of(M, 256) * tiles_of(out, 256) >= 64) {
             k_mx4_gemm_tile4<TY><<<tile_grid(tiles_of(M, 256) * tiles_of(out, 256)), 256, 0, st>>>(
                 (const uint8_t *)X, xs, M, nb, codes, scales, out, (TY *)Y);
             return hipGetLastError();
         }
         return split<TX, TY, 4, 4, 1>(X, xs, M, nb, codes, scales, out, Y, st);
     } else {
-        if (nb * 32 <= kTileMaxIn && tiles_of(M, 128) * tiles_of(out, 256) >= 128) {
+        const TX *const x = (const TX *)X;
+        TY *const y = (TY *)Y;
+        if (tiles_of(M, 128) * tiles_of(out, 256) >= 200)
             k_mx4_gemm_tile<TX, TY><<<tile_grid(tiles_of(M, 128) * tiles_of(out, 256)), 256, 0, st>>>(
-                (const TX *)X, M, nb, codes, scales, out, (TY *)Y);
-            return hipGetLastError();
-        }
-        return split<TX, TY, 4, 2, 1>(X, xs, M, nb, codes, scales, out, Y, st);
+                x, M, nb, codes, scales, out, y);
+        else if (M <= 32)
+            k_mx4_gemm_mid<TX, TY, 1><<<tile_grid(tiles_of(M, 32) * tiles_of(out, 64)), 512, 0, st>>>(
+                x, M, nb, codes, scales, out, y);
+        else
+            k_mx4_gemm_mid<TX, TY, 2><<<tile_grid(tiles_of(M, 64) * tiles_of(out, 64)), 512, 0, st>>>(
+                x, M, nb, codes, scales, out, y);
+        return hipGetLastError();
     }
 }
 

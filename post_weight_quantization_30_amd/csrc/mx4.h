@@ -307,7 +307,7 @@ template <int NT> struct StreamItem {
 };
 
 // A wave's 16 NT rows: scalar bases of the row tiles and one offset a lane (in
-// is at most 2^28 columns: 16 rows stay below 2^32 bytes).
+// is at most 2^23 columns: 16 rows stay below 2^32 bytes).
 template <int NT> struct StreamRows {
     const uint8_t *w[NT], *s[NT];
     uint32_t wo, so;
