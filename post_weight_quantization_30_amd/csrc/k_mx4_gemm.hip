@@ -20,72 +20,37 @@ __device__ __forceinline__ void store_tile(TY *Y, int64_t m, int64_t n, int64_t 
             Y[(m + i) * out + n] = static_cast<TY>(v[i]);
 }
 
-// Block: 16 MT tokens x 16 NT rows, the columns split over the waves in items
-// of 128 U; each wave's next item is in flight while it multiplies the
-// current one. The waves' sums are added in wave order through LDS.
-template <typename TX, typename TY, int MT, int NT, int U, int W>
-__global__ __launch_bounds__(64 * W) void k_mx4_gemm_split(const void *__restrict__ X, const uint8_t *__restrict__ xs,
-                                                           int64_t M, int nb, const uint8_t *__restrict__ codes,
+// Up to 16 tokens, 16-bit activations. Block: 16 rows, the columns split over W
+// waves in items of 128 U, each wave's next item in flight while it multiplies
+// the current one. The waves' sums are added in wave order through LDS.
+template <typename TX, typename TY, int U, int W>
+__global__ __launch_bounds__(64 * W) void k_mx4_gemm_split(const TX *__restrict__ X, int M, int nb,
+                                                           const uint8_t *__restrict__ codes,
                                                            const uint8_t *__restrict__ scales, int64_t out,
                                                            TY *__restrict__ Y)
 {
-    constexpr bool kAct4 = std::is_same<TX, Mx4Act>::value;
-    constexpr int TILES = MT * NT, TG = TILES < 4 ? TILES : 4;
-    __shared__ f32x4 red[W * TG * 64];
+    __shared__ f32x4 red[W * 64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, c = lane >> 4;
-    const int64_t n0 = (int64_t)blockIdx.x * (16 * NT), m0 = (int64_t)blockIdx.y * (16 * MT);
-
-    // rows past the ends load the last row: their results are not stored
-    Mx4Rows<TX, MT, NT> rows;
+    const int64_t n0 = (int64_t)blockIdx.x * 16, n = n0 + r < out ? n0 + r : out - 1;
+    const Mx4Rows<TX> rows = {codes + n * nb * 16, scales + n * nb, X + (int64_t)(r < M ? r : M - 1) * nb * 32};
+    f32x4 acc;
+    mx4_wave<U>(rows, acc, wave * (4 * U), W * (4 * U), nb, c);
+    red[wave * 64 + lane] = acc;
+    __syncthreads();
+    if (wave)
+        return;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        int64_t n = n0 + 16 * nt + r;
-        n = n < out ? n : out - 1;
-        rows.w[nt] = codes + n * nb * 16;
-        rows.ws[nt] = scales + n * nb;
-    }
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        int64_t m = m0 + 16 * mt + r;
-        m = m < M ? m : M - 1;
-        if constexpr (kAct4) {
-            rows.x[mt] = (const uint8_t *)X + m * nb * 16;
-            rows.xs[mt] = xs + m * nb;
-        } else {
-            rows.x[mt] = (const uint16_t *)X + m * nb * 32;
-            rows.xs[mt] = nullptr;
-        }
-    }
-
-    f32x4 acc[MT][NT];
-    mx4_wave<TX, MT, NT, U>(rows, acc, wave * (4 * U), W * (4 * U), nb, c);
-
-#pragma unroll
-    for (int t0 = 0; t0 < TILES; t0 += TG) {
-        if (t0)
-            __syncthreads();
-#pragma unroll
-        for (int t = 0; t < TG; ++t)
-            red[(wave * TG + t) * 64 + lane] = acc[(t0 + t) / NT][(t0 + t) % NT];
-        __syncthreads();
-        for (int idx = threadIdx.x; idx < TG * 64; idx += 64 * W) {
-            f32x4 sum = red[idx];
-#pragma unroll
-            for (int w = 1; w < W; ++w)
-                sum += red[w * TG * 64 + idx];
-            const int t = t0 + idx / 64, l = idx & 63;
-            store_tile<TX, TY>(Y, m0 + 16 * (t / NT) + 4 * (l >> 4), n0 + 16 * (t % NT) + (l & 15), M, out, sum);
-        }
-    }
+    for (int w = 1; w < W; ++w)
+        acc += red[w * 64 + lane];
+    store_tile<TX, TY>(Y, 4 * c, n0 + r, M, out, acc);
 }
 
-template <typename TX, typename TY, int MT, int NT, int U>
-hipError_t split(const void *X, const uint8_t *xs, int64_t M, int nb, const uint8_t *codes, const uint8_t *scales,
-                 int64_t out, void *Y, hipStream_t st)
+template <typename TX, typename TY, int U, int W>
+hipError_t split(const TX *X, int M, int nb, const uint8_t *codes, const uint8_t *scales, int64_t out, TY *Y,
+                 hipStream_t st)
 {
-    const dim3 grid((uint32_t)((out + 16 * NT - 1) / (16 * NT)), (uint32_t)((M + 16 * MT - 1) / (16 * MT)));
-    k_mx4_gemm_split<TX, TY, MT, NT, U, 8><<<grid, 512, 0, st>>>(X, xs, M, nb, codes, scales, out, (TY *)Y);
+    k_mx4_gemm_split<TX, TY, U, W><<<dim3((uint32_t)((out + 15) / 16)), 64 * W, 0, st>>>(X, M, nb, codes, scales, out, Y);
     return hipGetLastError();
 }
 
@@ -160,12 +125,12 @@ __global__ __launch_bounds__(512, 4) void k_mx4_gemv(const TX *__restrict__ X, i
 }
 
 template <typename TX, typename TY, int S>
-hipError_t gemv(const void *X, int M, int nb, const uint8_t *codes, const uint8_t *scales, int64_t out, void *Y,
+hipError_t gemv(const TX *X, int M, int nb, const uint8_t *codes, const uint8_t *scales, int64_t out, TY *Y,
                 hipStream_t st)
 {
     const int64_t tiles = (out + 15) / 16;
     k_mx4_gemv<TX, TY, S><<<dim3((uint32_t)((tiles + 8 / S - 1) / (8 / S))), 512, 0, st>>>(
-        (const TX *)X, M, nb, stream_chunk(M, nb), codes, scales, out, (TY *)Y);
+        X, M, nb, stream_chunk(M, nb), codes, scales, out, Y);
     return hipGetLastError();
 }
 
@@ -227,14 +192,35 @@ __device__ __forceinline__ void store_tiles(TY *__restrict__ Y, const f32x16 (&a
         }
 }
 
+// Eight scale bytes of a row from block b0 on, 127 for those past its end.
+__device__ __forceinline__ u32x2 load_scales8(const uint8_t *row, int b0, int nb)
+{
+    if (nb < 8 || b0 >= nb)
+        return u32x2{mx4_scales4(row, b0, nb), mx4_scales4(row, b0 + 4, nb)};
+    const int past = b0 + 8 > nb ? b0 + 8 - nb : 0;
+    uint64_t v;
+    __builtin_memcpy(&v, row + (b0 - past), 8);        // at any alignment
+    if (past)
+        v = v >> (8 * past) | 0x7F7F7F7F7F7F7F7Full << (64 - 8 * past);
+    return u32x2{(uint32_t)v, (uint32_t)(v >> 32)};
+}
+
+// The products below stage both operands through LDS, rows of eight 16-byte
+// chunks, chunk q of row m at position q ^ (m & 7): the eight rows that one
+// 128-byte LDS cycle serves then lie on distinct banks. A load unit takes 64
+// cycles for a load whose neighbouring lanes lie in different rows, as a matrix
+// operand wants them, whatever its width, and 19 where eight lanes cover 128
+// bytes (measured): weights read straight into operand registers, and scales a
+// byte or a word at a time, bounded these kernels by their loads.
+__device__ __forceinline__ int swizzled(int row, int q) { return row * 8 + (q ^ (row & 7)); }
+
 // 16-bit activations. Block: 128 tokens x 256 rows, 4 waves of 128 x 64. A
-// step is 64 columns: 128 bytes of every activation row go to LDS as eight
-// 16-byte chunks, chunk q of row m at position q ^ (m & 7), so that the eight
-// rows which one 128-byte LDS cycle serves lie on distinct banks. Weights go
-// from memory straight to the registers of the wave that multiplies them: no
-// other wave has its rows, and one conversion there serves all 128 tokens.
-// Step k + 1 is fetched while step k is multiplied; two LDS buffers, one
-// barrier a step.
+// step is 64 columns, 128 bytes of an activation row; weights come by the 256
+// columns (128 bytes of codes, 8 of scales) into one buffer that four steps
+// use. What comes next is on its way to registers meanwhile; activations have
+// two buffers, so a step costs one barrier, and a fourth one more. Weights are
+// converted by the wave that multiplies them (no other one has its rows), once
+// for 128 tokens.
 // Lane (r, h) = (lane % 32, lane / 32) of a 32-row tile holds in k-step s of 4
 // columns 32 h + 8 s ... of the step: chunk 4 h + s of an activation row, word
 // s of block h of a weight row.
@@ -246,8 +232,9 @@ __global__ __launch_bounds__(256, 2) void k_mx4_gemm_tile(const TX *__restrict__
 {
     typedef typename Vec8<TX>::type vec;
     constexpr int MT = 4, NT = 2, BM = 128, BN = 256;
-    constexpr int CH = BM * 8 / 256;                   // activation chunks a thread moves in a step
-    __shared__ __align__(16) u32x4 lds[2][BM * 8];
+    constexpr int CX = BM * 8 / 256, CW = BN * 8 / 256;        // chunks a thread moves
+    __shared__ __align__(16) u32x4 lx[2][BM * 8], lw[BN * 8];
+    __shared__ u32x2 lws[BN];
 
     int64_t m0, n0;
     if (!tile_of_block((M + BM - 1) / BM, (out + BN - 1) / BN, m0, n0))
@@ -266,61 +253,59 @@ __global__ __launch_bounds__(256, 2) void k_mx4_gemm_tile(const TX *__restrict__
     const uint8_t *const wbase = codes + n0 * nb * 16, *const wsbase = scales + n0 * nb;
     const uint32_t mlast = (uint32_t)(M - 1 - m0 < BM - 1 ? M - 1 - m0 : BM - 1);
     const uint32_t nlast = (uint32_t)(out - 1 - n0 < BN - 1 ? out - 1 - n0 : BN - 1);
-    uint32_t xo[CH], wo[NT], wso[NT];
-    int xdst[CH];
-    const int xq = threadIdx.x & 7;
+    const int q = threadIdx.x & 7, row0 = threadIdx.x >> 3;    // this thread's chunk of rows row0 + 32 i
+    uint32_t xo[CX], wo[CW];
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-        const uint32_t row = (threadIdx.x + i * 256) >> 3;
-        xdst[i] = row * 8 + (xq ^ (row & 7));
-        xo[i] = (row < mlast ? row : mlast) * (uint32_t)xrow + xq * 16;
+    for (int i = 0; i < CX; ++i) {
+        const uint32_t row = row0 + 32 * i;
+        xo[i] = (row < mlast ? row : mlast) * (uint32_t)xrow + q * 16;
     }
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        uint32_t n = 64 * wave + 32 * t + r;
-        n = n < nlast ? n : nlast;
-        wo[t] = n * (uint32_t)nb * 16 + h * 16;
-        wso[t] = n * (uint32_t)nb + h;
+    for (int i = 0; i < CW; ++i) {
+        const uint32_t row = row0 + 32 * i;
+        wo[i] = (row < nlast ? row : nlast) * (uint32_t)nb * 16 + q * 16;
     }
+    const uint32_t wso = (threadIdx.x < nlast ? threadIdx.x : nlast) * (uint32_t)nb;
+    const int dst = swizzled(row0, q);                 // rows 32 apart: 256 chunks apart, swizzled alike
 
     f32x16 acc[MT][NT];
-    u32x4 xr[CH], w[NT], wnext[NT];
-    uint32_t ws[NT], wsnext[NT];
+    u32x4 xr[CX], wr[CW];
+    u32x2 wsr, ws[NT];
     bool bad = false;
 
-    // An odd last block: the step's second half loads the row's last block
-    // instead; zeros (under scale 1) take its place on the way to use.
-    auto fetch = [&](int k) {
-        const bool end = k >= full;
-        const uint32_t xback = end && xq >= 4 ? 64 : 0, wback = end && h ? 1 : 0;
-        const uint8_t *const px = xbase + (int64_t)k * 128, *const pw = wbase + (int64_t)k * 32;
-        const uint8_t *const ps = wsbase + k * 2;
+    // Past a row's end (in its last step or stretch) the last chunk there is is
+    // loaded instead; zeros take its place among the activations, 127 (2^0)
+    // among the scales.
+    auto fetch_x = [&](int k) {
+        const uint32_t back = k >= full && q >= 4 ? 64 : 0;
+        const uint8_t *const p = xbase + (int64_t)k * 128;
 #pragma unroll
-        for (int i = 0; i < CH; ++i)
-            xr[i] = *reinterpret_cast<const u32x4 *>(px + (xo[i] - xback));
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            wnext[t] = *reinterpret_cast<const u32x4 *>(pw + (wo[t] - 16 * wback));
-            wsnext[t] = ps[wso[t] - wback];
-        }
+        for (int i = 0; i < CX; ++i)
+            xr[i] = *reinterpret_cast<const u32x4 *>(p + (xo[i] - back));
     };
-    auto stash = [&](int k) {
-        if (k >= full && xq >= 4)
+    auto stash_x = [&](int k) {
+        if (k >= full && q >= 4)
 #pragma unroll
-            for (int i = 0; i < CH; ++i)
+            for (int i = 0; i < CX; ++i)
                 xr[i] = u32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < CH; ++i)
-            lds[k & 1][xdst[i]] = xr[i];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            w[t] = wnext[t];
-            ws[t] = k >= full && h ? 127 : wsnext[t];
-        }
+        for (int i = 0; i < CX; ++i)
+            lx[k & 1][dst + 256 * i] = xr[i];
     };
-    auto xfrag = [&](int k, int t, int s) -> u32x4 {
-        const int row = 32 * t + r;
-        return lds[k & 1][row * 8 + ((4 * h + s) ^ (row & 7))];
+    auto fetch_w = [&](int j) {                        // columns 256 j ...
+        const int over = 8 * j + q - (nb - 1);
+        const uint32_t back = over > 0 ? over * 16 : 0;
+        const uint8_t *const p = wbase + (int64_t)j * 128;
+#pragma unroll
+        for (int i = 0; i < CW; ++i)
+            wr[i] = *reinterpret_cast<const u32x4 *>(p + (wo[i] - back));
+        wsr = load_scales8(wsbase + wso, 8 * j, nb);
+    };
+    auto stash_w = [&] {
+#pragma unroll
+        for (int i = 0; i < CW; ++i)
+            lw[dst + 256 * i] = wr[i];
+        lws[threadIdx.x] = wsr;
     };
     auto contract = [&]<bool WIDE>() {
 #pragma unroll
@@ -328,28 +313,45 @@ __global__ __launch_bounds__(256, 2) void k_mx4_gemm_tile(const TX *__restrict__
 #pragma unroll
             for (int b = 0; b < NT; ++b)
                 acc[a][b] = f32x16{};
-        fetch(0);
-        stash(0);
+        fetch_w(0);
+        fetch_x(0);
+        stash_w();
+        stash_x(0);
         __syncthreads();
         for (int k = 0; k < steps; ++k) {
+            const int part = k & 3;
+            if (part == 0) {
+                if (k + 4 < steps)
+                    fetch_w(k / 4 + 1);
+#pragma unroll
+                for (int b = 0; b < NT; ++b)
+                    ws[b] = lws[64 * wave + 32 * b + r];
+            }
             if (k + 1 < steps)
-                fetch(k + 1);
+                fetch_x(k + 1);
+            u32x4 w[NT];
+            uint32_t byte[NT];
+#pragma unroll
+            for (int b = 0; b < NT; ++b) {
+                w[b] = lw[swizzled(64 * wave + 32 * b + r, 2 * part + h)];
+                byte[b] = (part & 2 ? ws[b][1] : ws[b][0]) >> (16 * (part & 1) + 8 * h) & 0xFFu;
+                if constexpr (std::is_same<TX, f16>::value && !WIDE)
+                    bad = bad || !mx4_fits_f16(byte[b]);
+            }
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
                 if constexpr (!WIDE) {
                     vec wv[NT];
 #pragma unroll
                     for (int b = 0; b < NT; ++b) {
-                        if constexpr (std::is_same<TX, f16>::value) {
-                            wv[b] = mx4_to_f16(w[b][s], mx4_scale(ws[b]));
-                            bad = bad || !mx4_fits_f16(ws[b]);
-                        } else {
-                            wv[b] = mx4_to_bf16(w[b][s], mx4_scale(ws[b]));
-                        }
+                        if constexpr (std::is_same<TX, f16>::value)
+                            wv[b] = mx4_to_f16(w[b][s], mx4_scale(byte[b]));
+                        else
+                            wv[b] = mx4_to_bf16(w[b][s], mx4_scale(byte[b]));
                     }
 #pragma unroll
                     for (int a = 0; a < MT; ++a) {
-                        const vec x = __builtin_bit_cast(vec, xfrag(k, a, s));
+                        const vec x = __builtin_bit_cast(vec, lx[k & 1][swizzled(32 * a + r, 4 * h + s)]);
 #pragma unroll
                         for (int b = 0; b < NT; ++b)
                             acc[a][b] = mfma32(x, wv[b], acc[a][b]);
@@ -359,11 +361,11 @@ __global__ __launch_bounds__(256, 2) void k_mx4_gemm_tile(const TX *__restrict__
                     bf16x8 wv[NT];
 #pragma unroll
                     for (int b = 0; b < NT; ++b)
-                        wv[b] = mx4_to_bf16(w[b][s], mx4_scale(ws[b]));
+                        wv[b] = mx4_to_bf16(w[b][s], mx4_scale(byte[b]));
 #pragma unroll
                     for (int a = 0; a < MT; ++a) {
                         bf16x8 hi, lo;
-                        split_f16(__builtin_bit_cast(f16x8, xfrag(k, a, s)), hi, lo);
+                        split_f16(__builtin_bit_cast(f16x8, lx[k & 1][swizzled(32 * a + r, 4 * h + s)]), hi, lo);
 #pragma unroll
                         for (int b = 0; b < NT; ++b) {
                             acc[a][b] = mfma32(hi, wv[b], acc[a][b]);
@@ -374,8 +376,12 @@ __global__ __launch_bounds__(256, 2) void k_mx4_gemm_tile(const TX *__restrict__
                 }
             }
             if (k + 1 < steps)
-                stash(k + 1);
+                stash_x(k + 1);
             __syncthreads();
+            if (part == 3 && k + 1 < steps) {          // everyone has read the last of the weights
+                stash_w();
+                __syncthreads();
+            }
         }
     };
     contract.template operator()<false>();
@@ -387,13 +393,46 @@ __global__ __launch_bounds__(256, 2) void k_mx4_gemm_tile(const TX *__restrict__
     store_tiles<TY, MT, NT>(Y, acc, m0, n0 + 64 * wave, M, out, r, h);
 }
 
+// The sums of four groups of two waves (32 rows each), (0 + 2) + (1 + 3), to Y.
+template <typename TY, int MT>
+__device__ __forceinline__ void add_groups(float (&red)[2][32 * MT][64], f32x16 (&acc)[MT], int group, int wn, int r,
+                                           int h, TY *__restrict__ Y, int64_t m0, int64_t n0, int64_t M, int64_t out)
+{
+    auto put = [&](int g) {
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                red[g][32 * a + 8 * (i / 4) + 4 * h + i % 4][32 * wn + r] = acc[a][i];
+    };
+    if (group >= 2)
+        put(group - 2);
+    __syncthreads();
+    if (group < 2)
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                acc[a][i] += red[group][32 * a + 8 * (i / 4) + 4 * h + i % 4][32 * wn + r];
+    __syncthreads();
+    if (group < 2)
+        put(group);
+    __syncthreads();
+    const int n = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < 4 * MT; ++i) {
+        const int m = (threadIdx.x >> 6) + 8 * i;
+        const float sum = red[0][m][n] + red[1][m][n];
+        if (m0 + m < M && n0 + n < out)
+            Y[(m0 + m) * out + n0 + n] = static_cast<TY>(sum);
+    }
+}
+
 // 16-bit activations, too few 128 x 256 tiles for the chip. Block: 32 MT tokens
-// x 64 rows, 8 waves: two of 32 rows each in four groups that take the steps of
-// 64 columns in turn, each with its own LDS buffers (laid out as above); the
-// groups' sums meet in LDS. 64 x 64 tiles keep all units busy from about 200
-// tokens x 4000 rows on, and a token's row is read in whole 128-byte lines
-// (read in matrix order, 64 bytes of 16 rows at a time, it kept the load units
-// busy for twice as long as everything else took).
+// x 64 rows, 8 waves: two of 32 rows each in four groups. A round is 256
+// columns, of which each group takes 64; the groups' sums meet in LDS. Such
+// shapes leave one block or two on a unit, so a round's loads go out two rounds
+// ahead; one LDS buffer then does, and leaves room for the second block.
 template <typename TX, typename TY, int MT>
 __global__ __launch_bounds__(512, 4) void k_mx4_gemm_mid(const TX *__restrict__ X, int64_t M, int nb,
                                                          const uint8_t *__restrict__ codes,
@@ -402,8 +441,15 @@ __global__ __launch_bounds__(512, 4) void k_mx4_gemm_mid(const TX *__restrict__ 
 {
     typedef typename Vec8<TX>::type vec;
     constexpr int BM = 32 * MT, BN = 64, G = 4;
-    constexpr int CH = BM * 8 / 128;                   // activation chunks a thread moves in a step
-    __shared__ __align__(16) u32x4 lds[2][G][BM * 8];
+    constexpr int CX = BM * 8 / 128;                   // activation chunks a thread moves in a round
+    union Lds {
+        struct {
+            u32x4 x[G][BM * 8], w[BN * 8];
+            u32x2 ws[BN];
+        } in;
+        float red[G / 2][BM][BN];
+    };
+    __shared__ __align__(16) Lds lds;
 
     int64_t m0, n0;
     if (!tile_of_block((M + BM - 1) / BM, (out + BN - 1) / BN, m0, n0))
@@ -411,100 +457,102 @@ __global__ __launch_bounds__(512, 4) void k_mx4_gemm_mid(const TX *__restrict__ 
     m0 *= BM;
     n0 *= BN;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int r = lane & 31, h = lane >> 5, group = wave >> 1, wn = wave & 1, gt = threadIdx.x & 127;
+    const int r = lane & 31, h = lane >> 5, group = wave >> 1, wn = wave & 1;
     const int xrow = nb * 64;                          // bytes of an activation row
-    const int steps = (nb + 1) / 2, full = nb / 2;
+    const int rounds = (nb + 7) / 8;
 
+    // addresses and row ends as in k_mx4_gemm_tile
     const uint8_t *const xbase = (const uint8_t *)X + m0 * xrow;
     const uint8_t *const wbase = codes + n0 * nb * 16, *const wsbase = scales + n0 * nb;
     const uint32_t mlast = (uint32_t)(M - 1 - m0 < BM - 1 ? M - 1 - m0 : BM - 1);
     const uint32_t nlast = (uint32_t)(out - 1 - n0 < BN - 1 ? out - 1 - n0 : BN - 1);
-    uint32_t xo[CH];
-    int xdst[CH];
-    const int xq = gt & 7;
+    const int q = threadIdx.x & 7, xrow0 = (threadIdx.x & 127) >> 3;
+    const uint32_t wrow = threadIdx.x >> 3;
+    uint32_t xo[CX];
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-        const uint32_t row = (gt + i * 128) >> 3;
-        xdst[i] = row * 8 + (xq ^ (row & 7));
-        xo[i] = (row < mlast ? row : mlast) * (uint32_t)xrow + xq * 16;
+    for (int i = 0; i < CX; ++i) {
+        const uint32_t row = xrow0 + 16 * i;
+        xo[i] = (row < mlast ? row : mlast) * (uint32_t)xrow + q * 16;
     }
-    const uint32_t wr = 32 * wn + r, wrow = wr < nlast ? wr : nlast;
-    const uint32_t wo = wrow * (uint32_t)nb * 16 + h * 16, wso = wrow * (uint32_t)nb + h;
+    const uint32_t wo = (wrow < nlast ? wrow : nlast) * (uint32_t)nb * 16 + q * 16;
+    const uint32_t wso = (threadIdx.x < nlast ? threadIdx.x : nlast) * (uint32_t)nb;
 
     f32x16 acc[MT];
-    u32x4 xr[CH], w, wnext;
-    uint32_t ws, wsnext;
+    struct Round {
+        u32x4 x[CX], w;
+        u32x2 ws;
+    } even, odd;
     bool bad = false;
 
-    // steps past the last one are fetched as that one and dropped; for an odd
-    // last block see k_mx4_gemm_tile
-    auto fetch = [&](int k) {
-        k = k < steps ? k : steps - 1;
-        const bool end = k >= full;
-        const uint32_t xback = end && xq >= 4 ? 64 : 0, wback = end && h ? 1 : 0;
-        const uint8_t *const px = xbase + (int64_t)k * 128, *const pw = wbase + (int64_t)k * 32;
-        const uint8_t *const ps = wsbase + k * 2;
+    auto fetch = [&](Round &to, int j) {
+        if (j >= rounds)
+            return;
+        const int xb = 8 * j + 2 * group + (q >> 2), xover = (xb - (nb - 1)) * 64;     // its block of the row
+        const int wover = (8 * j + q - (nb - 1)) * 16;
+        const uint8_t *const px = xbase + (int64_t)j * 512 + group * 128, *const pw = wbase + (int64_t)j * 128;
 #pragma unroll
-        for (int i = 0; i < CH; ++i)
-            xr[i] = *reinterpret_cast<const u32x4 *>(px + (xo[i] - xback));
-        wnext = *reinterpret_cast<const u32x4 *>(pw + (wo - 16 * wback));
-        wsnext = ps[wso - wback];
+        for (int i = 0; i < CX; ++i)
+            to.x[i] = *reinterpret_cast<const u32x4 *>(px + ((int64_t)xo[i] - (xover > 0 ? xover : 0)));
+        to.w = *reinterpret_cast<const u32x4 *>(pw + ((int64_t)wo - (wover > 0 ? wover : 0)));
+        if (threadIdx.x < BN)
+            to.ws = load_scales8(wsbase + wso, 8 * j, nb);
     };
-    auto stash = [&](int k, int buf) {
-        if (k >= full && xq >= 4)
+    auto stash = [&](Round &from, int j) {
+        if (8 * j + 2 * group + (q >> 2) >= nb)
 #pragma unroll
-            for (int i = 0; i < CH; ++i)
-                xr[i] = u32x4{0, 0, 0, 0};
+            for (int i = 0; i < CX; ++i)
+                from.x[i] = u32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < CH; ++i)
-            lds[buf][group][xdst[i]] = xr[i];
-        w = wnext;
-        ws = k >= full && h ? 127 : wsnext;
+        for (int i = 0; i < CX; ++i)
+            lds.in.x[group][swizzled(xrow0 + 16 * i, q)] = from.x[i];
+        lds.in.w[swizzled(wrow, q)] = from.w;
+        if (threadIdx.x < BN)
+            lds.in.ws[threadIdx.x] = from.ws;
     };
     auto contract = [&]<bool WIDE>() {
 #pragma unroll
         for (int a = 0; a < MT; ++a)
             acc[a] = f32x16{};
-        fetch(group);
-        stash(group, 0);
-        __syncthreads();
-        int buf = 0;
-        for (int k0 = 0; k0 < steps; k0 += G, buf ^= 1) {
-            const int k = k0 + group;
-            const bool more = k0 + G < steps;
-            if (more)
-                fetch(k + G);
-            if (k < steps) {
+        auto round = [&](Round &now, int j) {
+            stash(now, j);
+            __syncthreads();
+            fetch(now, j + 2);
+            const u32x4 w = lds.in.w[swizzled(32 * wn + r, 2 * group + h)];
+            const u32x2 ws = lds.in.ws[32 * wn + r];
+            const uint32_t byte = (group & 2 ? ws[1] : ws[0]) >> (16 * (group & 1) + 8 * h) & 0xFFu;
+            if constexpr (std::is_same<TX, f16>::value && !WIDE)
+                bad = bad || !mx4_fits_f16(byte);
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    vec wv;
-                    bf16x8 wide;
+            for (int s = 0; s < 4; ++s) {
+                vec wv;
+                bf16x8 wide;
+                if constexpr (WIDE)
+                    wide = mx4_to_bf16(w[s], mx4_scale(byte));
+                else if constexpr (std::is_same<TX, f16>::value)
+                    wv = mx4_to_f16(w[s], mx4_scale(byte));
+                else
+                    wv = mx4_to_bf16(w[s], mx4_scale(byte));
+#pragma unroll
+                for (int a = 0; a < MT; ++a) {
+                    const u32x4 x = lds.in.x[group][swizzled(32 * a + r, 4 * h + s)];
                     if constexpr (WIDE) {
-                        wide = mx4_to_bf16(w[s], mx4_scale(ws));
-                    } else if constexpr (std::is_same<TX, f16>::value) {
-                        wv = mx4_to_f16(w[s], mx4_scale(ws));
-                        bad = bad || !mx4_fits_f16(ws);
+                        bf16x8 hi, lo;
+                        split_f16(__builtin_bit_cast(f16x8, x), hi, lo);
+                        acc[a] = mfma32(hi, wide, acc[a]);
+                        acc[a] = mfma32(lo, wide, acc[a]);
                     } else {
-                        wv = mx4_to_bf16(w[s], mx4_scale(ws));
-                    }
-#pragma unroll
-                    for (int a = 0; a < MT; ++a) {
-                        const int row = 32 * a + r;
-                        const u32x4 x = lds[buf][group][row * 8 + ((4 * h + s) ^ (row & 7))];
-                        if constexpr (WIDE) {
-                            bf16x8 hi, lo;
-                            split_f16(__builtin_bit_cast(f16x8, x), hi, lo);
-                            acc[a] = mfma32(hi, wide, acc[a]);
-                            acc[a] = mfma32(lo, wide, acc[a]);
-                        } else {
-                            acc[a] = mfma32(__builtin_bit_cast(vec, x), wv, acc[a]);
-                        }
+                        acc[a] = mfma32(__builtin_bit_cast(vec, x), wv, acc[a]);
                     }
                 }
             }
-            if (more)
-                stash(k + G, buf ^ 1);
             __syncthreads();
+        };
+        fetch(even, 0);
+        fetch(odd, 1);
+        for (int j = 0; j < rounds; j += 2) {
+            round(even, j);
+            if (j + 1 < rounds)
+                round(odd, j + 1);
         }
     };
     contract.template operator()<false>();
@@ -512,45 +560,32 @@ __global__ __launch_bounds__(512, 4) void k_mx4_gemm_mid(const TX *__restrict__ 
         if (__syncthreads_or(bad))                     // scales that fp16 cannot hold
             contract.template operator()<true>();
 
-    // the groups' sums, added in group order
-    float *const red = reinterpret_cast<float *>(lds);         // [G][BM][BN]
-#pragma unroll
-    for (int a = 0; a < MT; ++a)
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            red[(group * BM + 32 * a + 8 * (i / 4) + 4 * h + i % 4) * BN + 32 * wn + r] = acc[a][i];
-    __syncthreads();
-    const int n = threadIdx.x & (BN - 1);
-#pragma unroll
-    for (int q = 0; q < BM / 8; ++q) {
-        const int m = (threadIdx.x >> 6) + 8 * q;
-        float sum = red[m * BN + n];
-#pragma unroll
-        for (int g = 1; g < G; ++g)
-            sum += red[(g * BM + m) * BN + n];
-        if (m0 + m < M && n0 + n < out)
-            Y[(m0 + m) * out + n0 + n] = static_cast<TY>(sum);
-    }
+    add_groups<TY, MT>(lds.red, acc, group, wn, r, h, Y, m0, n0, M, out);
 }
 
-// MXFP4 activations. Block: 256 x 256, 4 waves of 128 x 128 (256 accumulator
-// registers each, one wave a SIMD). Both operands through LDS: a step is 128
-// columns, per row four 16-byte blocks and four scale bytes. Block q of row m
-// lies at position q ^ (m / 2 & 3) of the row's 64 bytes: eight rows at a time
-// fall on distinct banks. Three buffers: while step k is multiplied, k + 1 is
-// complete and k + 2 is on its way, so one barrier a step suffices and the
-// first operands of the next step can be read before it.
-// Lane (r, h) holds in k-step s of 2 block 2 s + h of its row.
+// The scale bytes h, h + 2, h + 4, h + 6 of eight: those of lane (r, h)'s blocks
+// in four k-steps, one register.
+__device__ __forceinline__ uint32_t own_scales(const u32x2 &s, int h)
+{
+    return __builtin_amdgcn_perm(s[1], s[0], 0x06040200u + 0x01010101u * (uint32_t)h);
+}
+
+// MXFP4 activations. Block: 256 x 256, 8 waves of 128 x 64. A stage is 256
+// columns, 128 bytes of codes and 8 of scales of every row, in one of two LDS
+// buffers; the next stage is on its way to registers while one is multiplied.
+// (Four waves of 128 x 128 read a third less from LDS, but alone on their SIMDs
+// they wait for it: 212 us against 1 .)
+// Lane (r, h) holds in k-step s of 4 block 2 s + h of its row.
 template <typename TY>
-__global__ __launch_bounds__(256, 1) void k_mx4_gemm_tile4(const uint8_t *__restrict__ xcodes,
+__global__ __launch_bounds__(512, 2) void k_mx4_gemm_tile4(const uint8_t *__restrict__ xcodes,
                                                            const uint8_t *__restrict__ xscales, int64_t M, int nb,
                                                            const uint8_t *__restrict__ codes,
                                                            const uint8_t *__restrict__ scales, int64_t out,
                                                            TY *__restrict__ Y)
 {
-    constexpr int MT = 4, NT = 4, B = 256, ST = 3;
-    __shared__ __align__(16) u32x4 lx[ST][B * 4], lw[ST][B * 4];
-    __shared__ uint32_t lxs[ST][B], lws[ST][B];
+    constexpr int MT = 4, NT = 2, B = 256, CH = 4;
+    __shared__ __align__(16) u32x4 lx[2][B * 8], lw[2][B * 8];
+    __shared__ u32x2 ls[2][2 * B];                     // scales: activation rows, then weight rows
 
     int64_t m0, n0;
     if (!tile_of_block((M + B - 1) / B, (out + B - 1) / B, m0, n0))
@@ -558,65 +593,52 @@ __global__ __launch_bounds__(256, 1) void k_mx4_gemm_tile4(const uint8_t *__rest
     m0 *= B;
     n0 *= B;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int r = lane & 31, h = lane >> 5, wm = wave >> 1, wn = wave & 1;
-    const int steps = (nb + 3) / 4, full = nb / 4;
+    const int r = lane & 31, h = lane >> 5, wm = wave >> 2, wn = wave & 3;
+    const int stages = (nb + 7) / 8;
 
+    // addresses as in k_mx4_gemm_tile
     const uint8_t *const xbase = xcodes + m0 * nb * 16, *const xsbase = xscales + m0 * nb;
     const uint8_t *const wbase = codes + n0 * nb * 16, *const wsbase = scales + n0 * nb;
     const uint32_t mlast = (uint32_t)(M - 1 - m0 < B - 1 ? M - 1 - m0 : B - 1);
     const uint32_t nlast = (uint32_t)(out - 1 - n0 < B - 1 ? out - 1 - n0 : B - 1);
-    const int q = threadIdx.x & 3;
-    uint32_t xo[4], wo[4];
-    int dst[4];
+    const int q = threadIdx.x & 7, row0 = threadIdx.x >> 3;    // this thread's chunk of rows row0 + 64 i
+    uint32_t xo[CH], wo[CH];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t row = (threadIdx.x + i * 256) >> 2;
-        dst[i] = row * 4 + (q ^ (row >> 1 & 3));
+    for (int i = 0; i < CH; ++i) {
+        const uint32_t row = row0 + 64 * i;
         xo[i] = (row < mlast ? row : mlast) * (uint32_t)nb * 16 + q * 16;
         wo[i] = (row < nlast ? row : nlast) * (uint32_t)nb * 16 + q * 16;
     }
-    const uint32_t srow = threadIdx.x;                 // the row whose scales this thread moves
-    const uint32_t xso = (srow < mlast ? srow : mlast) * (uint32_t)nb, wso = (srow < nlast ? srow : nlast) * (uint32_t)nb;
+    // the row whose scales this thread moves
+    const uint32_t srow = threadIdx.x & (B - 1), slast = threadIdx.x < B ? mlast : nlast;
+    const uint8_t *const sp = (threadIdx.x < B ? xsbase : wsbase) + (srow < slast ? srow : slast) * (uint32_t)nb;
+    const int dst = swizzled(row0, q);
 
-    u32x4 xr[4], wr[4];
-    uint32_t xsr, wsr;
-    // The last step of a row that ends inside it: zeros under scale 1 past the end.
+    u32x4 xr[CH], wr[CH];
+    u32x2 sr;
+    // past a row's end its last chunk is loaded; zeros, under scale 1, take its place
     auto fetch = [&](int k) {
-        const uint8_t *const px = xbase + (int64_t)k * 64, *const pw = wbase + (int64_t)k * 64;
-        const uint8_t *const pxs = xsbase + k * 4, *const pws = wsbase + k * 4;
-        if (k < full) {
+        const int over = 8 * k + q - (nb - 1);
+        const uint32_t back = over > 0 ? over * 16 : 0;
+        const uint8_t *const px = xbase + (int64_t)k * 128, *const pw = wbase + (int64_t)k * 128;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                xr[i] = *reinterpret_cast<const u32x4 *>(px + xo[i]);
-                wr[i] = *reinterpret_cast<const u32x4 *>(pw + wo[i]);
-            }
-            __builtin_memcpy(&xsr, pxs + xso, 4);
-            __builtin_memcpy(&wsr, pws + wso, 4);
-        } else {
-            const int valid = nb - 4 * k;              // 1 .. 3 blocks
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                xr[i] = wr[i] = u32x4{0, 0, 0, 0};
-                if (q < valid) {
-                    xr[i] = *reinterpret_cast<const u32x4 *>(px + xo[i]);
-                    wr[i] = *reinterpret_cast<const u32x4 *>(pw + wo[i]);
-                }
-            }
-            xsr = wsr = 0x7F7F7F7Fu;
-            for (int i = 0; i < valid; ++i) {
-                xsr = (xsr & ~(0xFFu << (8 * i))) | (uint32_t)pxs[xso + i] << (8 * i);
-                wsr = (wsr & ~(0xFFu << (8 * i))) | (uint32_t)pws[wso + i] << (8 * i);
-            }
+        for (int i = 0; i < CH; ++i) {
+            xr[i] = *reinterpret_cast<const u32x4 *>(px + (int64_t)(xo[i] - back));
+            wr[i] = *reinterpret_cast<const u32x4 *>(pw + (int64_t)(wo[i] - back));
         }
+        sr = load_scales8(sp, 8 * k, nb);
     };
-    auto stash = [&](int buf) {
+    auto stash = [&](int k) {
+        if (8 * k + q >= nb)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            lx[buf][dst[i]] = xr[i];
-            lw[buf][dst[i]] = wr[i];
+            for (int i = 0; i < CH; ++i)
+                xr[i] = wr[i] = u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            lx[k & 1][dst + 512 * i] = xr[i];
+            lw[k & 1][dst + 512 * i] = wr[i];
         }
-        lxs[buf][srow] = xsr;
-        lws[buf][srow] = wsr;
+        ls[k & 1][threadIdx.x] = sr;
     };
 
     f32x16 acc[MT][NT];
@@ -625,99 +647,236 @@ __global__ __launch_bounds__(256, 1) void k_mx4_gemm_tile4(const uint8_t *__rest
 #pragma unroll
         for (int b = 0; b < NT; ++b)
             acc[a][b] = f32x16{};
-    // this lane's rows: 128 wm + 32 a + r and 128 wn + 32 b + r; the swizzle
-    // depends on r alone
-    const int xr0 = (128 * wm + r) * 4, wr0 = (128 * wn + r) * 4, swz = r >> 1 & 3;
 
     fetch(0);
     stash(0);
-    if (steps > 1)
-        fetch(1);
     __syncthreads();
-    int cur = 0, nxt = 1;
-    for (int k = 0; k < steps; ++k) {
-        // step k + 1 (in registers) goes to its buffer, step k + 2 on its way
-        if (k + 1 < steps)
-            stash(nxt);
-        if (k + 2 < steps)
-            fetch(k + 2);
+    for (int k = 0; k < stages; ++k) {
+        if (k + 1 < stages)
+            fetch(k + 1);
         uint32_t sa[MT], sb[NT];
 #pragma unroll
         for (int a = 0; a < MT; ++a)
-            sa[a] = lxs[cur][128 * wm + 32 * a + r] >> (8 * h);
+            sa[a] = own_scales(ls[k & 1][128 * wm + 32 * a + r], h);
 #pragma unroll
         for (int b = 0; b < NT; ++b)
-            sb[b] = lws[cur][128 * wn + 32 * b + r] >> (8 * h);
+            sb[b] = own_scales(ls[k & 1][B + 64 * wn + 32 * b + r], h);
+        // k-step s + 1's operands are read while k-step s is multiplied
         u32x4 x[2][MT], w[2][NT];
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int p = (2 * s + h) ^ swz;
+        auto read = [&](int s) {
 #pragma unroll
             for (int a = 0; a < MT; ++a)
-                x[s][a] = lx[cur][xr0 + 128 * a + p];
+                x[s & 1][a] = lx[k & 1][swizzled(128 * wm + 32 * a + r, 2 * s + h)];
 #pragma unroll
             for (int b = 0; b < NT; ++b)
-                w[s][b] = lw[cur][wr0 + 128 * b + p];
-        }
+                w[s & 1][b] = lw[k & 1][swizzled(64 * wn + 32 * b + r, 2 * s + h)];
+        };
+        auto kstep = [&]<int S>() {
+            if (S < 3)
+                read(S + 1);
+            asm volatile("" ::: "memory");             // in this order: two sets of operands, no more
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int a = 0; a < MT; ++a)
+            for (int a = 0; a < MT; ++a)
 #pragma unroll
-            for (int b = 0; b < NT; ++b)
-                acc[a][b] = mfma32<0>(x[0][a], sa[a], w[0][b], sb[b], acc[a][b]);
+                for (int b = 0; b < NT; ++b)
+                    acc[a][b] = mfma32<S>(x[S & 1][a], sa[a], w[S & 1][b], sb[b], acc[a][b]);
+            // here, not after all reads of the stage (the products have no
+            // place of their own among the memory accesses)
 #pragma unroll
-        for (int a = 0; a < MT; ++a)
+            for (int a = 0; a < MT; ++a)
 #pragma unroll
-            for (int b = 0; b < NT; ++b)
-                acc[a][b] = mfma32<2>(x[1][a], sa[a], w[1][b], sb[b], acc[a][b]);
+                for (int b = 0; b < NT; ++b)
+                    asm volatile("" : "+v"(acc[a][b])::"memory");
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        read(0);
+        kstep.template operator()<0>();
+        kstep.template operator()<1>();
+        kstep.template operator()<2>();
+        kstep.template operator()<3>();
+        if (k + 1 < stages)
+            stash(k + 1);
         __syncthreads();
-        cur = nxt;
-        nxt = nxt == ST - 1 ? 0 : nxt + 1;
     }
-    store_tiles<TY, MT, NT>(Y, acc, m0 + 128 * wm, n0 + 128 * wn, M, out, r, h);
+    store_tiles<TY, MT, NT>(Y, acc, m0 + 128 * wm, n0 + 64 * wn, M, out, r, h);
+}
+
+// MXFP4 activations, too few 256 x 256 tiles for the chip, or few tokens. Block:
+// 32 MT tokens x 64 rows, 8 waves: two of 32 rows each in four groups. A round
+// is 1024 columns, of which each group takes 256; the groups' sums meet in LDS.
+template <typename TY, int MT>
+__global__ __launch_bounds__(512, 4) void k_mx4_gemm_mid4(const uint8_t *__restrict__ xcodes,
+                                                          const uint8_t *__restrict__ xscales, int64_t M, int nb,
+                                                          const uint8_t *__restrict__ codes,
+                                                          const uint8_t *__restrict__ scales, int64_t out,
+                                                          TY *__restrict__ Y)
+{
+    constexpr int BM = 32 * MT, BN = 64, G = 4, CX = BM / 16, CW = BN / 16;
+    union Lds {
+        struct {
+            u32x4 x[G][BM * 8], w[G][BN * 8];
+            u32x2 xs[G][BM], ws[G][BN];
+        } in;
+        float red[G / 2][BM][BN];
+    };
+    __shared__ __align__(16) Lds lds;
+
+    int64_t m0, n0;
+    if (!tile_of_block((M + BM - 1) / BM, (out + BN - 1) / BN, m0, n0))
+        return;
+    m0 *= BM;
+    n0 *= BN;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 31, h = lane >> 5, group = wave >> 1, wn = wave & 1;
+    const int rounds = (nb + 31) / 32;
+
+    // addresses as in k_mx4_gemm_tile; a group's 128 threads move its columns
+    const uint8_t *const xbase = xcodes + m0 * nb * 16, *const xsbase = xscales + m0 * nb;
+    const uint8_t *const wbase = codes + n0 * nb * 16, *const wsbase = scales + n0 * nb;
+    const uint32_t mlast = (uint32_t)(M - 1 - m0 < BM - 1 ? M - 1 - m0 : BM - 1);
+    const uint32_t nlast = (uint32_t)(out - 1 - n0 < BN - 1 ? out - 1 - n0 : BN - 1);
+    const int gt = threadIdx.x & 127, q = gt & 7, row0 = gt >> 3;      // chunk q of rows row0 + 16 i
+    uint32_t xo[CX], wo[CW];
+#pragma unroll
+    for (int i = 0; i < CX; ++i) {
+        const uint32_t row = row0 + 16 * i;
+        xo[i] = (row < mlast ? row : mlast) * (uint32_t)nb * 16 + q * 16;
+    }
+#pragma unroll
+    for (int i = 0; i < CW; ++i) {
+        const uint32_t row = row0 + 16 * i;
+        wo[i] = (row < nlast ? row : nlast) * (uint32_t)nb * 16 + q * 16;
+    }
+    // scales: the group's first BN threads a weight row each, the others an activation row
+    const uint32_t wso = ((uint32_t)gt < nlast ? (uint32_t)gt : nlast) * (uint32_t)nb;
+    const uint32_t xso = ((uint32_t)(gt - BN) < mlast ? (uint32_t)(gt - BN) : mlast) * (uint32_t)nb;
+
+    f32x16 acc[MT];
+#pragma unroll
+    for (int a = 0; a < MT; ++a)
+        acc[a] = f32x16{};
+    u32x4 xr[CX], wr[CW];
+    u32x2 sr;
+    auto fetch = [&](int j) {                          // zeros, under scale 1, past a row's end
+        const int b0 = 32 * j + 8 * group;             // the group's first block
+        const uint8_t *const px = xbase + (int64_t)b0 * 16, *const pw = wbase + (int64_t)b0 * 16;
+        if (b0 + 8 <= nb) {
+#pragma unroll
+            for (int i = 0; i < CX; ++i)
+                xr[i] = *reinterpret_cast<const u32x4 *>(px + xo[i]);
+#pragma unroll
+            for (int i = 0; i < CW; ++i)
+                wr[i] = *reinterpret_cast<const u32x4 *>(pw + wo[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < CX; ++i) {
+                xr[i] = u32x4{0, 0, 0, 0};
+                if (b0 + q < nb)
+                    xr[i] = *reinterpret_cast<const u32x4 *>(px + xo[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < CW; ++i) {
+                wr[i] = u32x4{0, 0, 0, 0};
+                if (b0 + q < nb)
+                    wr[i] = *reinterpret_cast<const u32x4 *>(pw + wo[i]);
+            }
+        }
+        if (gt < BN)
+            sr = load_scales8(wsbase + wso, b0, nb);
+        else if (gt < BN + BM)
+            sr = load_scales8(xsbase + xso, b0, nb);
+    };
+    fetch(0);
+    for (int j = 0; j < rounds; ++j) {
+        if (j)
+            __syncthreads();
+#pragma unroll
+        for (int i = 0; i < CX; ++i)
+            lds.in.x[group][swizzled(row0 + 16 * i, q)] = xr[i];
+#pragma unroll
+        for (int i = 0; i < CW; ++i)
+            lds.in.w[group][swizzled(row0 + 16 * i, q)] = wr[i];
+        if (gt < BN)
+            lds.in.ws[group][gt] = sr;
+        else if (gt < BN + BM)
+            lds.in.xs[group][gt - BN] = sr;
+        __syncthreads();
+        if (j + 1 < rounds)
+            fetch(j + 1);
+        uint32_t sa[MT];
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+            sa[a] = own_scales(lds.in.xs[group][32 * a + r], h);
+        const uint32_t sb = own_scales(lds.in.ws[group][32 * wn + r], h);
+        auto kstep = [&]<int S>() {
+            const u32x4 w = lds.in.w[group][swizzled(32 * wn + r, 2 * S + h)];
+#pragma unroll
+            for (int a = 0; a < MT; ++a)
+                acc[a] = mfma32<S>(lds.in.x[group][swizzled(32 * a + r, 2 * S + h)], sa[a], w, sb, acc[a]);
+        };
+        kstep.template operator()<0>();
+        kstep.template operator()<1>();
+        kstep.template operator()<2>();
+        kstep.template operator()<3>();
+    }
+    __syncthreads();
+    add_groups<TY, MT>(lds.red, acc, group, wn, r, h, Y, m0, n0, M, out);
 }
 
 inline int64_t tiles_of(int64_t n, int64_t size) { return (n + size - 1) / size; }
 // Whole multiples of 8: see tile_of_block.
 inline uint32_t tile_grid(int64_t tiles) { return (uint32_t)((tiles + 7) / 8 * 8); }
 
-template <typename TX, typename TY>
-hipError_t gemm(const void *X, const uint8_t *xs, int64_t M, int nb, const uint8_t *codes, const uint8_t *scales,
-                int64_t out, void *Y, hipStream_t st)
+// Whether 64-token tiles of 64 rows beat 32-token ones: a block's time is about
+// 1 to 0.6, and a unit does its blocks one after another.
+inline bool mid_by_64(int64_t M, int64_t out)
 {
-    if constexpr (!std::is_same<TX, Mx4Act>::value) {
+    const int64_t n = tiles_of(out, 64), two = tiles_of(tiles_of(M, 64) * n, 256), one = tiles_of(tiles_of(M, 32) * n, 256);
+    return M > 32 && two * 10 <= one * 6;
+}
+
+template <typename TX, typename TY>
+hipError_t gemm(const TX *X, int64_t M, int nb, const uint8_t *codes, const uint8_t *scales, int64_t out, TY *Y,
+                hipStream_t st)
+{
+    if (M <= 16) {
         // Enough row tiles for more than a block's worth a unit: few waves a
         // tile (28672 rows of 4096, 4 tokens: S = 1, 2, 4, 8 take 16.4, 15.7,
         // 17.9, 21.1 us; 12288 rows, 2 tokens: 14.4, 10.3, 9.7, 10.9).
-        const int64_t tiles = (out + 15) / 16;
-        if (M <= 16 && tiles >= 640) {
-            if (tiles >= 1280)
-                return gemv<TX, TY, 2>(X, (int)M, nb, codes, scales, out, Y, st);
+        const int64_t tiles = tiles_of(out, 16);
+        if (tiles >= 1280)
+            return gemv<TX, TY, 2>(X, (int)M, nb, codes, scales, out, Y, st);
+        if (tiles >= 640)
             return gemv<TX, TY, 4>(X, (int)M, nb, codes, scales, out, Y, st);
-        }
+        return split<TX, TY, 4, 8>(X, (int)M, nb, codes, scales, out, Y, st);
     }
-    if (M <= 16)
-        return split<TX, TY, 1, 1, 4>(X, xs, M, nb, codes, scales, out, Y, st);
-    if constexpr (std::is_same<TX, Mx4Act>::value) {
-        if (tiles_of(M, 256) * tiles_of(out, 256) >= 64) {
-            k_mx4_gemm_tile4<TY><<<tile_grid(tiles_of(M, 256) * tiles_of(out, 256)), 256, 0, st>>>(
-                (const uint8_t *)X, xs, M, nb, codes, scales, out, (TY *)Y);
-            return hipGetLastError();
-        }
-        return split<TX, TY, 4, 4, 1>(X, xs, M, nb, codes, scales, out, Y, st);
-    } else {
-        const TX *const x = (const TX *)X;
-        TY *const y = (TY *)Y;
-        if (tiles_of(M, 128) * tiles_of(out, 256) >= 200)
-            k_mx4_gemm_tile<TX, TY><<<tile_grid(tiles_of(M, 128) * tiles_of(out, 256)), 256, 0, st>>>(
-                x, M, nb, codes, scales, out, y);
-        else if (M <= 32)
-            k_mx4_gemm_mid<TX, TY, 1><<<tile_grid(tiles_of(M, 32) * tiles_of(out, 64)), 512, 0, st>>>(
-                x, M, nb, codes, scales, out, y);
-        else
-            k_mx4_gemm_mid<TX, TY, 2><<<tile_grid(tiles_of(M, 64) * tiles_of(out, 64)), 512, 0, st>>>(
-                x, M, nb, codes, scales, out, y);
-        return hipGetLastError();
-    }
+    if (tiles_of(M, 128) * tiles_of(out, 256) >= 200)
+        k_mx4_gemm_tile<TX, TY><<<tile_grid(tiles_of(M, 128) * tiles_of(out, 256)), 256, 0, st>>>(X, M, nb, codes, scales,
+                                                                                                out, Y);
+    else if (mid_by_64(M, out))
+        k_mx4_gemm_mid<TX, TY, 2><<<tile_grid(tiles_of(M, 64) * tiles_of(out, 64)), 512, 0, st>>>(X, M, nb, codes, scales,
+                                                                                                out, Y);
+    else
+        k_mx4_gemm_mid<TX, TY, 1><<<tile_grid(tiles_of(M, 32) * tiles_of(out, 64)), 512, 0, st>>>(X, M, nb, codes, scales,
+                                                                                                out, Y);
+    return hipGetLastError();
+}
+
+template <typename TY>
+hipError_t gemm_a4(const uint8_t *xc, const uint8_t *xs, int64_t M, int nb, const uint8_t *codes, const uint8_t *scales,
+                   int64_t out, TY *Y, hipStream_t st)
+{
+    if (tiles_of(M, 256) * tiles_of(out, 256) >= 64)
+        k_mx4_gemm_tile4<TY><<<tile_grid(tiles_of(M, 256) * tiles_of(out, 256)), 512, 0, st>>>(xc, xs, M, nb, codes,
+                                                                                             scales, out, Y);
+    else if (mid_by_64(M, out))
+        k_mx4_gemm_mid4<TY, 2><<<tile_grid(tiles_of(M, 64) * tiles_of(out, 64)), 512, 0, st>>>(xc, xs, M, nb, codes,
+                                                                                             scales, out, Y);
+    else
+        k_mx4_gemm_mid4<TY, 1><<<tile_grid(tiles_of(M, 32) * tiles_of(out, 64)), 512, 0, st>>>(xc, xs, M, nb, codes,
+                                                                                             scales, out, Y);
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -727,10 +886,10 @@ hipError_t launch_mx4_gemm(const void *X, int dtype, int64_t M, int64_t in, cons
 {
     const int nb = (int)(in / kMxBlock);
     if (dtype == AWQ_F16)
-        return yf32 ? gemm<f16, float>(X, nullptr, M, nb, codes, scales, out, Y, st)
-                    : gemm<f16, f16>(X, nullptr, M, nb, codes, scales, out, Y, st);
-    return yf32 ? gemm<bf16, float>(X, nullptr, M, nb, codes, scales, out, Y, st)
-                : gemm<bf16, bf16>(X, nullptr, M, nb, codes, scales, out, Y, st);
+        return yf32 ? gemm((const f16 *)X, M, nb, codes, scales, out, (float *)Y, st)
+                    : gemm((const f16 *)X, M, nb, codes, scales, out, (f16 *)Y, st);
+    return yf32 ? gemm((const bf16 *)X, M, nb, codes, scales, out, (float *)Y, st)
+                : gemm((const bf16 *)X, M, nb, codes, scales, out, (bf16 *)Y, st);
 }
 
 hipError_t launch_mx4_gemm_a4(const uint8_t *xcodes, const uint8_t *xscales, int64_t M, int64_t in,
@@ -739,9 +898,9 @@ hipError_t launch_mx4_gemm_a4(const uint8_t *xcodes, const uint8_t *xscales, int
 {
     const int nb = (int)(in / kMxBlock);
     switch (y_dtype) {
-    case AWQ_F32: return gemm<Mx4Act, float>(xcodes, xscales, M, nb, codes, scales, out, Y, st);
-    case AWQ_F16: return gemm<Mx4Act, f16>(xcodes, xscales, M, nb, codes, scales, out, Y, st);
-    default: return gemm<Mx4Act, bf16>(xcodes, xscales, M, nb, codes, scales, out, Y, st);
+    case AWQ_F32: return gemm_a4(xcodes, xscales, M, nb, codes, scales, out, (float *)Y, st);
+    case AWQ_F16: return gemm_a4(xcodes, xscales, M, nb, codes, scales, out, (f16 *)Y, st);
+    default: return gemm_a4(xcodes, xscales, M, nb, codes, scales, out, (bf16 *)Y, st);
     }
 }
 

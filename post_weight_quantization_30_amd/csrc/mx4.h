@@ -28,17 +28,6 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kMxBlock = 32;
 
-// The activations of a product: 16-bit values, or MXFP4 like the weights.
-struct Mx4Act {};
-
-template <typename TX> struct XFrag {                 // one block of one row, one lane
-    typename Vec8<TX>::type v[4];
-};
-template <> struct XFrag<Mx4Act> {
-    u32x4 q;
-    uint32_t s;
-};
-
 // 2^(byte - 127) as the conversion instructions take it: they read the
 // exponent field only, 0 as 2^-127 and 255 as NaN.
 __device__ __forceinline__ float mx4_scale(uint32_t byte) { return __builtin_bit_cast(float, byte << 23); }
@@ -100,23 +89,6 @@ __device__ __forceinline__ f32x4 mx4_mfma(const f16x8 &a, const f16x8 &b, const 
 {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
-// Both operands MXFP4: 128 columns, a lane's block and its scale byte (the
-// low byte of each scale register).
-__device__ __forceinline__ f32x4 mx4_mfma(const u32x4 &a, uint32_t sa, const u32x4 &b, uint32_t sb, const f32x4 &c)
-{
-    const i32x8 a8 = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
-    const i32x8 b8 = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, c, 4, 4, 0, (int)sa, 0, (int)sb);
-}
-
-// What one wave loads at a time: U steps of 128 columns of 16 NT weight rows
-// and 16 MT activation rows.
-template <typename TX, int MT, int NT, int U> struct Mx4Item {
-    u32x4 w[NT][U];
-    uint32_t ws[NT][U];            // the four blocks' scale bytes
-    XFrag<TX> x[MT][U];
-};
-
 // The scale bytes of blocks b .. b + 3 of a row (127 for those past its end).
 __device__ __forceinline__ uint32_t mx4_scales4(const uint8_t *row, int b, int nb)
 {
@@ -131,119 +103,6 @@ __device__ __forceinline__ uint32_t mx4_scales4(const uint8_t *row, int b, int n
     return v;
 }
 
-// A lane's rows: pointers to the starts of their codes, scales and activations.
-template <typename TX, int MT, int NT> struct Mx4Rows {
-    const uint8_t *w[NT], *ws[NT];
-    const void *x[MT];
-    const uint8_t *xs[MT];         // activation scales (MXFP4 activations only)
-};
-
-// Loads the item whose first block is b0. Blocks past the row's end load its
-// last block: compute drops them.
-template <typename TX, int MT, int NT, int U>
-__device__ __forceinline__ void mx4_load(Mx4Item<TX, MT, NT, U> &it, const Mx4Rows<TX, MT, NT> &rows, int b0, int nb,
-                                         int c)
-{
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int b4 = b0 + 4 * u, b = b4 + c < nb ? b4 + c : nb - 1;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            it.w[nt][u] = *reinterpret_cast<const u32x4 *>(rows.w[nt] + (int64_t)b * 16);
-            it.ws[nt][u] = mx4_scales4(rows.ws[nt], b4, nb);
-        }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            if constexpr (std::is_same<TX, Mx4Act>::value) {
-                it.x[mt][u].q = *reinterpret_cast<const u32x4 *>((const uint8_t *)rows.x[mt] + (int64_t)b * 16);
-                it.x[mt][u].s = mx4_scales4(rows.xs[mt], b4, nb);
-            } else {
-#pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const int bs = b4 + s < nb ? b4 + s : nb - 1;
-                    it.x[mt][u].v[s] = load8((const TX *)rows.x[mt] + (int64_t)bs * 32 + 8 * c);
-                }
-            }
-        }
-    }
-}
-
-// acc += the item's products. Blocks past the row's end: their steps are left
-// out (16-bit activations), or zeros under scale 1 multiply (MXFP4). WIDE is
-// for fp16 activations under scales that fp16 cannot hold: weights in bf16,
-// activations as two bf16 parts. The plain form reports such scales in `bad`.
-template <bool WIDE, typename TX, int MT, int NT, int U>
-__device__ __forceinline__ void mx4_compute(Mx4Item<TX, MT, NT, U> &it, f32x4 (&acc)[MT][NT], int b0, int nb, int c,
-                                            bool &bad)
-{
-    if constexpr (std::is_same<TX, Mx4Act>::value) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (b0 + 4 * u + 4 > nb && b0 + 4 * u + c >= nb) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    it.w[nt][u] = u32x4{0, 0, 0, 0};
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-                    it.x[mt][u].q = u32x4{0, 0, 0, 0};
-            }
-            uint32_t sx[MT];
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-                sx[mt] = it.x[mt][u].s >> (8 * c);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const uint32_t sw = it.ws[nt][u] >> (8 * c);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-                    acc[mt][nt] = mx4_mfma(it.x[mt][u].q, sx[mt], it.w[nt][u], sw, acc[mt][nt]);
-            }
-        }
-    } else {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                transpose4(it.w[nt][u]);
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                if (b0 + 4 * u + s >= nb)
-                    break;
-                if constexpr (!WIDE) {
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const uint32_t byte = it.ws[nt][u] >> (8 * s) & 0xFFu;
-                        typename Vec8<TX>::type w;
-                        if constexpr (std::is_same<TX, f16>::value) {
-                            w = mx4_to_f16(it.w[nt][u][s], mx4_scale(byte));
-                            bad = bad || !mx4_fits_f16(byte);
-                        } else {
-                            w = mx4_to_bf16(it.w[nt][u][s], mx4_scale(byte));
-                        }
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt)
-                            acc[mt][nt] = mx4_mfma(it.x[mt][u].v[s], w, acc[mt][nt]);
-                    }
-                } else {
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        __builtin_amdgcn_sched_barrier(0);   // one split at a time: registers
-                        bf16x8 hi, lo;
-                        split_f16(it.x[mt][u].v[s], hi, lo);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            const bf16x8 w =
-                                mx4_to_bf16(it.w[nt][u][s], mx4_scale(it.ws[nt][u] >> (8 * s) & 0xFFu));
-                            acc[mt][nt] = mx4_mfma(hi, w, acc[mt][nt]);
-                            acc[mt][nt] = mx4_mfma(lo, w, acc[mt][nt]);
-                        }
-                    }
-                }
-            }
-        }
-    }
-}
-
 template <int MT, int NT> __device__ __forceinline__ void mx4_zero(f32x4 (&acc)[MT][NT])
 {
 #pragma unroll
@@ -253,43 +112,102 @@ template <int MT, int NT> __device__ __forceinline__ void mx4_zero(f32x4 (&acc)[
             acc[mt][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
 }
 
-// One wave's share of a contraction: the items that begin at blocks first,
-// first + step, ... of the rows, each in flight while the one before it is
-// multiplied. fp16 activations: where a scale turns out not to fit, all of it
-// once more in the wide form (real weights never need it, so the hot loop
-// carries no branch and no registers for it).
-template <typename TX, int MT, int NT, int U>
-__device__ __forceinline__ void mx4_wave(const Mx4Rows<TX, MT, NT> &rows, f32x4 (&acc)[MT][NT], int first, int step,
-                                         int nb, int c)
+// ---------------------------------------------------------------------------
+// The direct form, for few rows: a wave's share of a contraction, operands
+// straight from memory to registers. A lane's rows: the starts of its codes,
+// scales and activations.
+template <typename TX> struct Mx4Rows {
+    const uint8_t *w, *ws;
+    const TX *x;
+};
+template <typename TX, int U> struct Mx4Item {         // U steps of 128 columns of 16 rows and 16 tokens
+    u32x4 w[U];
+    uint32_t ws[U];                                    // the four blocks' scale bytes
+    typename Vec8<TX>::type x[U][4];
+};
+
+// Loads the item whose first block is b0. Blocks past the row's end load its
+// last block: compute leaves them out.
+template <typename TX, int U>
+__device__ __forceinline__ void mx4_load(Mx4Item<TX, U> &it, const Mx4Rows<TX> &rows, int b0, int nb, int c)
 {
-    mx4_zero(acc);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int b4 = b0 + 4 * u, b = b4 + c < nb ? b4 + c : nb - 1;
+        it.w[u] = *reinterpret_cast<const u32x4 *>(rows.w + (int64_t)b * 16);
+        it.ws[u] = mx4_scales4(rows.ws, b4, nb);
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+            it.x[u][s] = load8(rows.x + (int64_t)(b4 + s < nb ? b4 + s : nb - 1) * 32 + 8 * c);
+    }
+}
+
+// acc += the item's products. WIDE is for fp16 activations under scales that
+// fp16 cannot hold: weights in bf16, activations as two bf16 parts. The plain
+// form reports such scales in `bad`.
+template <bool WIDE, typename TX, int U>
+__device__ __forceinline__ void mx4_compute(Mx4Item<TX, U> &it, f32x4 &acc, int b0, int nb, bool &bad)
+{
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        transpose4(it.w[u]);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            if (b0 + 4 * u + s >= nb)
+                break;
+            const uint32_t byte = it.ws[u] >> (8 * s) & 0xFFu;
+            if constexpr (WIDE) {
+                __builtin_amdgcn_sched_barrier(0);           // one split at a time: registers
+                bf16x8 hi, lo;
+                split_f16(it.x[u][s], hi, lo);
+                const bf16x8 w = mx4_to_bf16(it.w[u][s], mx4_scale(byte));
+                acc = mx4_mfma(hi, w, acc);
+                acc = mx4_mfma(lo, w, acc);
+            } else if constexpr (std::is_same<TX, f16>::value) {
+                acc = mx4_mfma(it.x[u][s], mx4_to_f16(it.w[u][s], mx4_scale(byte)), acc);
+                bad = bad || !mx4_fits_f16(byte);
+            } else {
+                acc = mx4_mfma(it.x[u][s], mx4_to_bf16(it.w[u][s], mx4_scale(byte)), acc);
+            }
+        }
+    }
+}
+
+// The items that begin at blocks first, first + step, ... of the rows, each in
+// flight while the one before it is multiplied. fp16 activations: where a scale
+// turns out not to fit, all of it once more in the wide form (real weights
+// never need it, so the hot loop carries no branch and no registers for it).
+template <int U, typename TX>
+__device__ __forceinline__ void mx4_wave(const Mx4Rows<TX> &rows, f32x4 &acc, int first, int step, int nb, int c)
+{
+    acc = f32x4{0.f, 0.f, 0.f, 0.f};
     if (first >= nb)
         return;
-    Mx4Item<TX, MT, NT, U> a, b;
+    Mx4Item<TX, U> a, b;
     bool bad = false;
     int i = first;
     mx4_load(a, rows, i, nb, c);
     while (true) {
         if (i + step < nb)
             mx4_load(b, rows, i + step, nb, c);
-        mx4_compute<false>(a, acc, i, nb, c, bad);
+        mx4_compute<false>(a, acc, i, nb, bad);
         i += step;
         if (i >= nb)
             break;
         if (i + step < nb)
             mx4_load(a, rows, i + step, nb, c);
-        mx4_compute<false>(b, acc, i, nb, c, bad);
+        mx4_compute<false>(b, acc, i, nb, bad);
         i += step;
         if (i >= nb)
             break;
     }
     if constexpr (std::is_same<TX, f16>::value) {
         if (__any(bad)) {
-            mx4_zero(acc);
+            acc = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
             for (i = first; i < nb; i += step) {
                 mx4_load(a, rows, i, nb, c);
-                mx4_compute<true>(a, acc, i, nb, c, bad);
+                mx4_compute<true>(a, acc, i, nb, bad);
             }
         }
     }
