@@ -172,37 +172,63 @@ __device__ __forceinline__ bool tile_of_block(int64_t tm, int64_t tn, int64_t &m
     return true;
 }
 
-// The results of a wave's MT x NT tiles, tile (a, b) at token m0 + 32 a, row
+// The results of a wave's MT x 2 tiles, tile (a, b) at token m0 + 32 a, row
 // n0 + 32 b: register i of lane (r, h) is token 8 (i / 4) + 4 h + i % 4, row r.
-template <typename TY, int MT, int NT>
-__device__ __forceinline__ void store_tiles(TY *__restrict__ Y, const f32x16 (&acc)[MT][NT], int64_t m0, int64_t n0,
-                                            int64_t M, int64_t out, int r, int h)
+// They go through 8 KB of the wave's own LDS, 32 tokens at a time, and out in
+// 16-byte pieces, 64 rows of a token together: a store of single values in the
+// matrix layout keeps the store unit busy for as long as a 16-byte one.
+template <typename TY, int MT>
+__device__ __forceinline__ void store_tiles(TY *__restrict__ Y, const f32x16 (&acc)[MT][2], float *lds, int64_t m0,
+                                            int64_t n0, int64_t M, int64_t out, int lane)
 {
+    constexpr int V = 16 / sizeof(TY);                 // values a piece
+    typedef TY piece __attribute__((ext_vector_type(V)));
+    const int r = lane & 31, h = lane >> 5;
 #pragma unroll
-    for (int a = 0; a < MT; ++a)
+    for (int a = 0; a < MT; ++a) {
+        // value (t, n) at 64 t + (n ^ (8 (t & 4))): lane halves, 4 tokens apart, use different banks
 #pragma unroll
-        for (int b = 0; b < NT; ++b) {
-            const int64_t n = n0 + 32 * b + r;
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const int64_t m = m0 + 32 * a + 8 * (i / 4) + 4 * h + i % 4;
-                if (m < M && n < out)
-                    Y[m * out + n] = static_cast<TY>(acc[a][b][i]);
+                const int t = 8 * (i / 4) + 4 * h + i % 4;
+                lds[64 * t + ((32 * b + r) ^ (8 * (t & 4)))] = acc[a][b][i];
+            }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int k = 0; k < 32 * 64 / V / 64; ++k) {
+            const int p = lane + 64 * k, t = p / (64 / V), n = p % (64 / V) * V;
+            piece v;
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                v[e] = static_cast<TY>(lds[64 * t + ((n ^ (8 * (t & 4))) + e)]);
+            const int64_t m = m0 + 32 * a + t;
+            TY *const y = Y + m * out + n0 + n;
+            if (m < M) {
+                if (n0 + n + V <= out)
+                    __builtin_memcpy(y, &v, 16);       // at any alignment
+                else
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        if (n0 + n + e < out)
+                            y[e] = v[e];
             }
         }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
 }
 
 // Eight scale bytes of a row from block b0 on, 127 for those past its end.
 __device__ __forceinline__ u32x2 load_scales8(const uint8_t *row, int b0, int nb)
 {
-    if (nb < 8 || b0 >= nb)
-        return u32x2{mx4_scales4(row, b0, nb), mx4_scales4(row, b0 + 4, nb)};
-    const int past = b0 + 8 > nb ? b0 + 8 - nb : 0;
-    uint64_t v;
-    __builtin_memcpy(&v, row + (b0 - past), 8);        // at any alignment
-    if (past)
-        v = v >> (8 * past) | 0x7F7F7F7F7F7F7F7Full << (64 - 8 * past);
-    return u32x2{(uint32_t)v, (uint32_t)(v >> 32)};
+    u32x2 v;
+    if (b0 + 8 <= nb)
+        __builtin_memcpy(&v, row + b0, 8);             // at any alignment
+    else
+        v = u32x2{mx4_scales4(row, b0, nb), mx4_scales4(row, b0 + 4, nb)};
+    return v;
 }
 
 // The products below stage both operands through LDS, rows of eight 16-byte
@@ -390,7 +416,8 @@ __global__ __launch_bounds__(256, 2) void k_mx4_gemm_tile(const TX *__restrict__
     if constexpr (std::is_same<TX, f16>::value)
         if (__syncthreads_or(bad))
             contract.template operator()<true>();
-    store_tiles<TY, MT, NT>(Y, acc, m0, n0 + 64 * wave, M, out, r, h);
+    // every wave is past its last read of the operands
+    store_tiles<TY, MT>(Y, acc, reinterpret_cast<float *>(lx) + 2048 * wave, m0, n0 + 64 * wave, M, out, lane);
 }
 
 // The sums of four groups of two waves (32 rows each), (0 + 2) + (1 + 3), to Y.
@@ -571,10 +598,11 @@ __device__ __forceinline__ uint32_t own_scales(const u32x2 &s, int h)
 }
 
 // MXFP4 activations. Block: 256 x 256, 8 waves of 128 x 64. A stage is 256
-// columns, 128 bytes of codes and 8 of scales of every row, in one of two LDS
-// buffers; the next stage is on its way to registers while one is multiplied.
-// (Four waves of 128 x 128 read a third less from LDS, but alone on their SIMDs
-// they wait for it: 212 us against 1 .)
+// columns, 128 bytes of codes of every row, in one of two LDS buffers; scales
+// come by four stages, 32 bytes of a row, into one buffer (a load of scales
+// costs a load unit the same whatever its width). What comes next is on its way
+// to registers meanwhile. (Four waves of 128 x 128 read a third less from LDS,
+// but alone on their SIMDs they wait for it.)
 // Lane (r, h) holds in k-step s of 4 block 2 s + h of its row.
 template <typename TY>
 __global__ __launch_bounds__(512, 2) void k_mx4_gemm_tile4(const uint8_t *__restrict__ xcodes,
@@ -585,7 +613,7 @@ __global__ __launch_bounds__(512, 2) void k_mx4_gemm_tile4(const uint8_t *__rest
 {
     constexpr int MT = 4, NT = 2, B = 256, CH = 4;
     __shared__ __align__(16) u32x4 lx[2][B * 8], lw[2][B * 8];
-    __shared__ u32x2 ls[2][2 * B];                     // scales: activation rows, then weight rows
+    __shared__ u32x2 ls[4][2 * B];                     // scales: activation rows, then weight rows
 
     int64_t m0, n0;
     if (!tile_of_block((M + B - 1) / B, (out + B - 1) / B, m0, n0))
@@ -615,7 +643,7 @@ __global__ __launch_bounds__(512, 2) void k_mx4_gemm_tile4(const uint8_t *__rest
     const int dst = swizzled(row0, q);
 
     u32x4 xr[CH], wr[CH];
-    u32x2 sr;
+    u32x2 sr[4];
     // past a row's end its last chunk is loaded; zeros, under scale 1, take its place
     auto fetch = [&](int k) {
         const int over = 8 * k + q - (nb - 1);
@@ -626,7 +654,16 @@ __global__ __launch_bounds__(512, 2) void k_mx4_gemm_tile4(const uint8_t *__rest
             xr[i] = *reinterpret_cast<const u32x4 *>(px + (int64_t)(xo[i] - back));
             wr[i] = *reinterpret_cast<const u32x4 *>(pw + (int64_t)(wo[i] - back));
         }
-        sr = load_scales8(sp, 8 * k, nb);
+    };
+    auto fetch_s = [&](int k) {                        // of stages k ... k + 3
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            sr[i] = load_scales8(sp, 8 * (k + i), nb);
+    };
+    auto stash_s = [&] {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            ls[i][threadIdx.x] = sr[i];
     };
     auto stash = [&](int k) {
         if (8 * k + q >= nb)
@@ -638,7 +675,6 @@ __global__ __launch_bounds__(512, 2) void k_mx4_gemm_tile4(const uint8_t *__rest
             lx[k & 1][dst + 512 * i] = xr[i];
             lw[k & 1][dst + 512 * i] = wr[i];
         }
-        ls[k & 1][threadIdx.x] = sr;
     };
 
     f32x16 acc[MT][NT];
@@ -649,18 +685,22 @@ __global__ __launch_bounds__(512, 2) void k_mx4_gemm_tile4(const uint8_t *__rest
             acc[a][b] = f32x16{};
 
     fetch(0);
+    fetch_s(0);
     stash(0);
+    stash_s();
     __syncthreads();
     for (int k = 0; k < stages; ++k) {
         if (k + 1 < stages)
             fetch(k + 1);
+        if ((k & 3) == 0 && k + 4 < stages)
+            fetch_s(k + 4);
         uint32_t sa[MT], sb[NT];
 #pragma unroll
         for (int a = 0; a < MT; ++a)
-            sa[a] = own_scales(ls[k & 1][128 * wm + 32 * a + r], h);
+            sa[a] = own_scales(ls[k & 3][128 * wm + 32 * a + r], h);
 #pragma unroll
         for (int b = 0; b < NT; ++b)
-            sb[b] = own_scales(ls[k & 1][B + 64 * wn + 32 * b + r], h);
+            sb[b] = own_scales(ls[k & 3][B + 64 * wn + 32 * b + r], h);
         // k-step s + 1's operands are read while k-step s is multiplied
         u32x4 x[2][MT], w[2][NT];
         auto read = [&](int s) {
@@ -698,8 +738,13 @@ __global__ __launch_bounds__(512, 2) void k_mx4_gemm_tile4(const uint8_t *__rest
         if (k + 1 < stages)
             stash(k + 1);
         __syncthreads();
+        if ((k & 3) == 3 && k + 1 < stages) {          // everyone has read the last of the scales
+            stash_s();
+            __syncthreads();
+        }
     }
-    store_tiles<TY, MT, NT>(Y, acc, m0 + 128 * wm, n0 + 64 * wn, M, out, r, h);
+    // every wave is past its last read of the operands
+    store_tiles<TY, MT>(Y, acc, reinterpret_cast<float *>(lx) + 2048 * wave, m0 + 128 * wm, n0 + 64 * wn, M, out, lane);
 }
 
 // MXFP4 activations, too few 256 x 256 tiles for the chip, or few tokens. Block:
@@ -851,7 +896,12 @@ hipError_t gemm(const TX *X, int64_t M, int nb, const uint8_t *codes, const uint
             return gemv<TX, TY, 4>(X, (int)M, nb, codes, scales, out, Y, st);
         return split<TX, TY, 4, 8>(X, (int)M, nb, codes, scales, out, Y, st);
     }
-    if (tiles_of(M, 128) * tiles_of(out, 256) >= 200)
+    // 128 x 256 tiles or 64 x 64 ones: 4096 columns take 31 us for up to 512 of
+    // the small tiles and each further 512; large ones 80 us for up to 256 (one
+    // a unit), 100 for each 512 (1024 x 4096 rows: 60 us small, 80 large; 2048 x
+    // 4096: 120, 79)
+    const int64_t large = tiles_of(M, 128) * tiles_of(out, 256), small = tiles_of(tiles_of(M, 64) * tiles_of(out, 64), 512);
+    if ((large <= 256 ? 80 : 100 * tiles_of(large, 512)) < 31 * small)
         k_mx4_gemm_tile<TX, TY><<<tile_grid(tiles_of(M, 128) * tiles_of(out, 256)), 256, 0, st>>>(X, M, nb, codes, scales,
                                                                                                 out, Y);
     else if (mid_by_64(M, out))
@@ -867,7 +917,10 @@ template <typename TY>
 hipError_t gemm_a4(const uint8_t *xc, const uint8_t *xs, int64_t M, int nb, const uint8_t *codes, const uint8_t *scales,
                    int64_t out, TY *Y, hipStream_t st)
 {
-    if (tiles_of(M, 256) * tiles_of(out, 256) >= 64)
+    // 256 x 256 tiles or 64 x 64 ones: 4096 columns take 40 us for each 256 of the
+    // large, 13 for each 512 of the small (1024 x 4096 rows: 26 us small, 38
+    // large; 2048 x 4096: 52, 40)
+    if (3 * tiles_of(tiles_of(M, 256) * tiles_of(out, 256), 256) < tiles_of(tiles_of(M, 64) * tiles_of(out, 64), 512))
         k_mx4_gemm_tile4<TY><<<tile_grid(tiles_of(M, 256) * tiles_of(out, 256)), 512, 0, st>>>(xc, xs, M, nb, codes,
                                                                                              scales, out, Y);
     else if (mid_by_64(M, out))

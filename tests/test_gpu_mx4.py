@@ -157,7 +157,8 @@ def operands(awq, M, out, n, dt, seed):
 # inside a wave's share, more items than waves, several token and row tiles
 GEMM = [(1, 1, 32), (1, 300, 512), (2, 17, 96), (5, 64, 4096), (16, 48, 608), (15, 1000, 14336), (17, 130, 1024),
         (33, 65, 32), (64, 64, 2080), (70, 20, 256), (200, 515, 1120), (256, 4096, 512), (257, 511, 544),
-        (1000, 700, 1056), (515, 3000, 128), (2100, 4100, 160), (2047, 4097, 544), (4100, 2050, 32)]
+        (1000, 700, 1056), (515, 3000, 128), (2100, 4100, 160), (2047, 4097, 544), (4100, 2050, 32),
+        (4, 20490, 160), (16, 10250, 608), (1, 10241, 96)]
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
@@ -196,14 +197,14 @@ def test_gemm_a4(awq, case, dt):
     assert torch.equal(Y, awq.mx4_gemm_a4(xcd, xsd, cd, sd, dtype=DT[dt]))
 
 
-@pytest.mark.parametrize("M,out", [(3, 130), (40, 130), (300, 130), (1030, 4100)])
+@pytest.mark.parametrize("M,out,n", [(3, 130, 672), (40, 130, 672), (300, 130, 672), (1030, 4100, 672),
+                                     (16, 10250, 2208), (5, 20490, 4704), (1, 70, 14368)])
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
-def test_gemm_any_scale(awq, M, out, dt):
+def test_gemm_any_scale(awq, M, out, n, dt):
     """Random codes under scales far outside fp16's range (and row to row different
     ones), fp16 activations up to their largest and down to subnormal ones."""
-    say("any scale", M, out, dt)
+    say("any scale", M, out, n, dt)
     r = np.random.default_rng(7)
-    n = 672
     c = r.integers(0, 256, (out, n // 2)).astype(np.uint8)
     base = np.where(np.arange(out) % 3 == 0, 127, r.integers(40, 200, out))
     s = (base[:, None] + r.integers(-20, 21, (out, n // 32))).clip(0, 254).astype(np.uint8)
@@ -214,7 +215,7 @@ def test_gemm_any_scale(awq, M, out, dt):
     check(Y, X64 @ Wd.T, np.abs(X64) @ np.abs(Wd).T, n, "f32", "any scale")
 
 
-@pytest.mark.parametrize("M,out", [(1, 130), (40, 130), (300, 130), (2050, 2050)])
+@pytest.mark.parametrize("M,out", [(1, 130), (40, 130), (300, 130), (2050, 4100)])
 def test_gemm_a4_any_scale(awq, M, out):
     say("a4 any scale", M, out)
     r = np.random.default_rng(8)
@@ -227,7 +228,7 @@ def test_gemm_a4_any_scale(awq, M, out):
     check(awq.mx4_gemm_a4(*d, dtype=torch.float32), Xq @ Wd.T, np.abs(Xq) @ np.abs(Wd).T, n, "f32", "a4 any scale")
 
 
-@pytest.mark.parametrize("M,out", [(1, 70), (40, 70), (300, 70), (2100, 4100)])
+@pytest.mark.parametrize("M,out", [(1, 70), (40, 70), (300, 70), (2100, 4100), (3, 10250), (2, 20490)])
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
 @pytest.mark.parametrize("n", [96, 1024])
 def test_nan_and_infinity_stay_in_their_rows(awq, M, out, dt, n):
