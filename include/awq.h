@@ -380,8 +380,8 @@ int awq_mx4_gemm_a4(const uint8_t *xcodes, const uint8_t *xscales, int64_t M, in
  *   lowest index; a NaN ranks lowest); p = softmax(l) over all experts at those,
  *   divided by their sum if renorm is not 0;
  *   h_e = silu(Wgate_e x) * (Wup_e x);  y = sum_e p_e Wdown_e h_e.
- * p_e h_e is rounded once to `dtype`, the type in which the layer's matrix
- * products take their activations; everything else is fp32 up to Y.
+ * Everything is fp32 up to Y but p_e h_e, which keeps 16 significant bits (and
+ * fp32's range).
  *   X:      device (M, hidden) of `dtype` (AWQ_F16 or AWQ_BF16), M <= AWQ_MX4_MOE_MAX_TOKENS.
  *   router: device (experts, hidden) of `dtype`.
  *   gu_codes, gu_scales: device, the MXFP4 matrix (experts * 2 * inter, hidden): of each

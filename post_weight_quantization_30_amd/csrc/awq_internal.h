@@ -304,19 +304,39 @@ hipError_t launch_mx4_gemm(const void *X, int dtype, int64_t M, int64_t in, cons
 hipError_t launch_mx4_gemm_a4(const uint8_t *xcodes, const uint8_t *xscales, int64_t M, int64_t in,
                               const uint8_t *codes, const uint8_t *scales, int64_t out, void *Y, int y_dtype,
                               hipStream_t st);
-// Parts that the down product's contraction is shared out to: with fewer than
-// 256 tiles of 16 hidden columns as many as keep every unit busy, but no part
-// without 16 waves' worth of 512-column units (`groups`: of one
-// expert's 16 tokens at most, as many as there can be).
-inline int mx4_moe_parts(int64_t hidden, int64_t inter, int64_t groups)
+// How the down product of awq_mx4_moe is launched (see k_mx4_moe_down): blocks
+// over the hidden columns, parts of the contraction. `groups`: of one expert's
+// 16 tokens at most, as many as there can be; more of them never make fewer
+// parts.
+struct Mx4DownPlan {
+    bool wide;
+    int waves, blocks, parts;
+};
+inline Mx4DownPlan mx4_down_plan(int64_t M, int64_t hidden, int64_t inter, int64_t groups)
 {
-    const int64_t fill = 256 / (hidden / 16), work = groups * ((inter + 511) / 512) / 32;
-    const int64_t z = fill < work ? fill : work;
-    return (int)(z < 1 ? 1 : z > 8 ? 8 : z);
+    const int64_t tiles = hidden / 16, units = groups * ((inter + 511) / 512);
+    Mx4DownPlan p;
+    p.wide = M > 4;
+    int64_t parts;
+    if (!p.wide) {
+        p.waves = 16;
+        p.blocks = (int)tiles;
+        parts = units / 32 < 256 / tiles ? units / 32 : 256 / tiles;       // 16 waves' worth of units or more
+    } else {
+        // the number of waves, 8 to 16, that leaves the fewest without columns
+        p.waves = tiles <= 8 ? 8 : tiles < 16 ? (int)tiles : 16;
+        for (int w = p.waves - 1; w >= 8; --w)
+            if ((tiles + w - 1) / w * w < (tiles + p.waves - 1) / p.waves * p.waves)
+                p.waves = w;
+        p.blocks = (int)((tiles + p.waves - 1) / p.waves);
+        parts = units / 4 < 256 / p.blocks ? units / 4 : 256 / p.blocks;   // four units a wave or more
+    }
+    p.parts = (int)(parts < 1 ? 1 : parts > 64 ? 64 : parts);
+    return p;
 }
 // Workspace of awq_mx4_moe: the routed experts and their weights, (M, top_k),
-// p h of every pair, (M top_k, inter) in the activations' type, the logits and
-// the parts' fp32 sums.
+// p h of every pair as two bf16 parts, (M top_k, 2, inter), the logits and the
+// parts' fp32 sums.
 struct Mx4MoeWs {
     size_t ids_off, w_off, h_off, logits_off, sums_off, total;
 };
@@ -324,11 +344,11 @@ inline Mx4MoeWs mx4_moe_ws_layout(int64_t M, int64_t hidden, int64_t inter, int 
 {
     Mx4MoeWs w;
     const size_t pairs = (size_t)(M * top_k);
-    const int parts = mx4_moe_parts(hidden, inter, M * top_k + M * top_k / 16);    // any number of experts
+    const int parts = mx4_down_plan(M, hidden, inter, M * top_k + M * top_k / 16).parts;   // any number of experts
     w.ids_off = 0;
     w.w_off = align256(pairs * sizeof(int32_t));
     w.h_off = w.w_off + align256(pairs * sizeof(float));
-    w.logits_off = w.h_off + align256(pairs * (size_t)inter * 2);
+    w.logits_off = w.h_off + align256(pairs * (size_t)inter * 4);
     w.sums_off = w.logits_off + align256((size_t)M * AWQ_MX4_MOE_MAX_EXPERTS * sizeof(float));
     w.total = w.sums_off + (parts > 1 ? align256((size_t)parts * (size_t)(M * hidden) * sizeof(float)) : 0);
     return w;

@@ -101,7 +101,7 @@ __global__ __launch_bounds__(512, 4) void k_mx4_gemv(const TX *__restrict__ X, i
 #pragma unroll 1
             for (; i < end; i += S) {
                 const TX *const x[1] = {(const TX *)(lds + row + (i - i0) * kStreamBlocks * 64)};
-                stream_compute<WIDE, true>(it, x, acc, nb - i * kStreamBlocks, 1, rows,
+                stream_compute<WIDE, true>(it, x, acc, nb - i * kStreamBlocks, rows,
                                      i + S < items ? (i + S) * kStreamBlocks : -1, nb, c, bad);
             }
         }

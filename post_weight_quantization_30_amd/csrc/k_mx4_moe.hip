@@ -221,7 +221,7 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void k_mx4_moe_up(const TX *__res
                                                                  const float *__restrict__ weights,
                                                                  const uint8_t *__restrict__ codes,
                                                                  const uint8_t *__restrict__ scales,
-                                                                 TX *__restrict__ h)
+                                                                 bf16 *__restrict__ h)
 {
     __shared__ Routed rt;
     __shared__ __align__(16) uint8_t lds[kStreamLds + 16 * 16];
@@ -267,7 +267,7 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void k_mx4_moe_up(const TX *__res
                 if (i + S < items)
                     stream_load(next, rows, (i + S) * kStreamBlocks, nb, c);
                 const TX *const x[1] = {(const TX *)(lds + xrow + (i - i0) * kStreamBlocks * 64)};
-                stream_compute<WIDE, false>(cur, x, acc, nb - i * kStreamBlocks, 1, rows, -1, nb, c, bad);
+                stream_compute<WIDE, false>(cur, x, acc, nb - i * kStreamBlocks, rows, -1, nb, c, bad);
                 i += S;
             };
             while (i < end) {
@@ -308,52 +308,51 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void k_mx4_moe_up(const TX *__res
                 const int pair = list[4 * c + k];
                 const float gate = acc[0][0][k], up = acc[0][1][k];
                 const float v = gate / (1.0f + expf(-gate)) * up * weights[pair];
-                h[(int64_t)pair * inter + col0 + r] = static_cast<TX>(v);
+                // two bf16 parts: 16 significant bits (an infinity stays in the first)
+                const float hi = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, v) & 0xFFFF0000u);
+                bf16 *const out = h + (int64_t)pair * 2 * inter + col0 + r;
+                out[0] = static_cast<bf16>(hi);
+                out[inter] = static_cast<bf16>(v == hi ? 0.0f : v - hi);
             }
         }
     }
 }
 
 // ---- down -------------------------------------------------------------------
-// Block: 16 hidden columns, all tokens, 16 waves. The contraction is a list of
-// units, 512 columns of one group's expert each, by group and column. A unit's
-// activations are one row of 1 KB for each of the group's tokens; a stage is as
-// many units as have ROWS rows at most, in one of two LDS buffers, and the
-// waves take its units in turn. A stage's rows are on their way to registers
+// The contraction is a list of units, 512 columns of one group's expert each, by
+// group and column. A unit's activations are one row (1 KB of each part) for
+// each of the group's tokens; a stage is as many units as have ROWS rows at
+// most, in one of two LDS buffers. A stage's rows are on their way to registers
 // while the one before it is multiplied, and so are every wave's next weights,
 // across the stages' barriers. A unit's results, one row for each of its
 // tokens, go to the wave's own sums of all tokens in LDS: an expert's NaN
-// reaches its own tokens only, and the order of all additions is fixed. With
-// few hidden columns the units are shared out over gridDim.y blocks, whose fp32
-// sums k_mx4_moe_sum adds (`sums`: (gridDim.y, M, hidden)).
-constexpr int kRowBytes = 64 * kStreamBlocks + 16;     // of a row in LDS, padded (see stream_chunk)
-constexpr int kDownWaves = 16;
+// reaches its own tokens only, and the order of all additions is fixed. The
+// units are shared out over gridDim.y blocks, whose fp32 sums k_mx4_moe_sum
+// adds (`sums`: (gridDim.y, M, hidden)).
+//
+// Two ways to use a block's waves:
+//   narrow: 16 hidden columns, the waves take a stage's units in turn. Nothing
+//     is read ahead of need and every block starts with all of its loads, which
+//     suits the smallest calls.
+//   wide: 16 hidden columns a wave, each wave all units: the staged rows serve
+//     all waves, which is what counts once tokens have more bytes than weights.
+constexpr int kPartBytes = 64 * kStreamBlocks, kRowBytes = 2 * kPartBytes + 16;    // in LDS, padded (see stream_chunk)
 
-template <typename TX, int TOK, int ROWS>
-__global__ __launch_bounds__(64 * kDownWaves) void k_mx4_moe_down(const TX *__restrict__ h, int M, int hidden, int inter,
-                                                                  int top_k, const int32_t *__restrict__ ids,
-                                                                  const uint8_t *__restrict__ codes,
-                                                                  const uint8_t *__restrict__ scales,
-                                                                  TX *__restrict__ Y, float *__restrict__ sums)
-{
-    constexpr int kRegs = (ROWS + kDownWaves - 1) / kDownWaves;    // rows a wave moves in a stage
-    __shared__ __align__(16) uint8_t bufs[2][ROWS * kRowBytes];
-    __shared__ float out[kDownWaves][TOK * 16];
-    __shared__ Routed rt;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int r = lane & 15, c = lane >> 4;
-    read_routing(rt, ids, M * top_k, top_k);
-    const int groups = __builtin_amdgcn_readfirstlane(rt.groups);
-    const int nb = inter / kMxBlock, per = (nb + kStreamBlocks - 1) / kStreamBlocks;   // units of a group
+// Rows in unit order: group g's begin at per * begin[g], unit i's at + i *
+// size. A stage: units u0 ... u0 + units - 1, rows r0 ... r0 + rows - 1.
+struct Stage {                                         // uniform
+    int u0, units, r0, rows;
+};
 
-    // Rows in unit order: group g's begin at per * begin[g], unit i's at + i *
-    // size. A stage: units u0 ... u0 + units - 1, rows r0 ... r0 + rows - 1.
-    struct Stage {                                     // uniform
-        int u0, units, r0, rows;
-    };
-    const int first_unit = (int)((int64_t)per * groups * blockIdx.y / gridDim.y);
-    const int end_unit = (int)((int64_t)per * groups * (blockIdx.y + 1) / gridDim.y);
-    auto open = [&](Stage &s, int u0) {
+template <int ROWS, int WAVES> struct DownRows {
+    static constexpr int kRegs = (ROWS + WAVES - 1) / WAVES;       // rows a wave moves in a stage, at WAVES or more
+    const Routed &rt;
+    const bf16 *const h;
+    const int nb, per, groups, end_unit, waves, wave, lane;
+    u32x4 pre[kRegs][2];
+
+    __device__ __forceinline__ void open(Stage &s, int u0) const
+    {
         s.u0 = u0;
         s.units = s.rows = s.r0 = 0;
         if (u0 >= end_unit)
@@ -378,108 +377,147 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_mx4_moe_down(const TX *__re
         }
         if (s.units > end_unit - u0)                   // the rows past the last unit are moved, not used
             s.units = end_unit - u0;
-    };
-    u32x4 pre[kRegs];
-    auto fetch = [&](const Stage &s) {
+    }
+    __device__ __forceinline__ void fetch(const Stage &s)
+    {
 #pragma unroll
         for (int q = 0; q < kRegs; ++q)
-            if (wave + q * kDownWaves < s.rows) {
-                const int R = s.r0 + wave + q * kDownWaves, at = R / per;      // `at` lies among the group's pairs
+            if (wave + q * waves < s.rows) {
+                const int R = s.r0 + wave + q * waves, at = R / per;           // `at` lies among the group's pairs
                 const int g = __builtin_amdgcn_readfirstlane(rt.group_of[at]), size = rt.size(g);
                 const int begin = __builtin_amdgcn_readfirstlane(rt.begin[g]);
                 const int local = R - per * begin, i = local / size;
                 const int p = __builtin_amdgcn_readfirstlane(rt.pairs[begin + local - i * size]);
-                if (lane < (nb - i * kStreamBlocks) * 4)
-                    pre[q] = *reinterpret_cast<const u32x4 *>(h + ((int64_t)p * nb + i * kStreamBlocks) * 32 + lane * 8);
+                const bf16 *const src = h + ((int64_t)p * 2 * nb + i * kStreamBlocks) * 32 + lane * 8;
+                if (lane < (nb - i * kStreamBlocks) * 4) {
+                    pre[q][0] = *reinterpret_cast<const u32x4 *>(src);
+                    pre[q][1] = *reinterpret_cast<const u32x4 *>(src + nb * 32);
+                }
             }
-    };
-    auto stash = [&](const Stage &s, uint8_t *buf) {   // lanes past a row's end store what nothing reads
+    }
+    __device__ __forceinline__ void stash(const Stage &s, uint8_t *buf) const
+    {                                                  // lanes past a row's end store what nothing reads
 #pragma unroll
         for (int q = 0; q < kRegs; ++q)
-            if (wave + q * kDownWaves < s.rows)
-                *reinterpret_cast<u32x4 *>(buf + (wave + q * kDownWaves) * kRowBytes + lane * 16) = pre[q];
-    };
+            if (wave + q * waves < s.rows)
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+                    *reinterpret_cast<u32x4 *>(buf + (wave + q * waves) * kRowBytes + part * kPartBytes + lane * 16) =
+                        pre[q][part];
+    }
+};
+
+template <typename TY, int TOK, int ROWS, bool WIDE>
+__global__ __launch_bounds__(1024) void k_mx4_moe_down(const bf16 *__restrict__ h, int M, int hidden, int inter,
+                                                       int top_k, const int32_t *__restrict__ ids,
+                                                       const uint8_t *__restrict__ codes,
+                                                       const uint8_t *__restrict__ scales, TY *__restrict__ Y,
+                                                       float *__restrict__ sums)
+{
+    constexpr int kWaves = 16;                         // wide: at most, and 8 at least
+    __shared__ __align__(16) uint8_t bufs[2][ROWS * kRowBytes];
+    __shared__ float out[kWaves][TOK * 16];
+    __shared__ Routed rt;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 15, c = lane >> 4, waves = WIDE ? (int)(blockDim.x >> 6) : kWaves;
+    read_routing(rt, ids, M * top_k, top_k);
+    const int groups = __builtin_amdgcn_readfirstlane(rt.groups);
+    const int nb = inter / kMxBlock, per = (nb + kStreamBlocks - 1) / kStreamBlocks;   // units of a group
+    const int first_unit = (int)((int64_t)per * groups * blockIdx.y / gridDim.y);
+    const int end_unit = (int)((int64_t)per * groups * (blockIdx.y + 1) / gridDim.y);
+    DownRows<ROWS, WIDE ? 8 : kWaves> act{rt, h, nb, per, groups, end_unit, waves, wave, lane, {}};
+
+    const int tiles = hidden / 16;
+    int tile = WIDE ? (int)blockIdx.x * waves + wave : (int)blockIdx.x;
+    const bool idle = tile >= tiles;                   // wide: no columns left for this wave
+    tile = idle ? tiles - 1 : tile;
     StreamRows<1> rows;
     rows.lane(r, c, nb);
     auto aim = [&](int u) -> int {                     // rows of the unit's expert; the unit's first block
         const int g = u / per;
-        const int64_t row = (int64_t)__builtin_amdgcn_readfirstlane(rt.expert[g]) * hidden + blockIdx.x * 16;
+        const int64_t row = (int64_t)__builtin_amdgcn_readfirstlane(rt.expert[g]) * hidden + tile * 16;
         rows.w[0] = codes + row * nb * 16;
         rows.s[0] = scales + row * nb;
         return (u - g * per) * kStreamBlocks;
     };
-    bool bad = false;
 
-    auto contract = [&]<bool WIDE>() {
-        for (int k = lane; k < TOK * 16; k += 64)
-            out[wave][k] = 0.f;
-        Stage cur, nxt;
-        open(cur, first_unit);
-        fetch(cur);
-        StreamItem<1> it;                              // the wave's next unit, if `loaded`
-        bool loaded = wave < cur.units;
-        if (loaded)
-            stream_load(it, rows, aim(first_unit + wave), nb, c);
-        stash(cur, bufs[0]);
-        open(nxt, cur.u0 + cur.units);
-        fetch(nxt);
-        __syncthreads();
-        uint8_t *now = bufs[0], *then = bufs[1];
-#pragma unroll 1
-        while (cur.units) {
-#pragma unroll 1
-            for (int j = wave; j < cur.units; j += kDownWaves) {
-                const int u = cur.u0 + j, g = u / per, i = u - g * per;
-                const int count = rt.size(g), begin = __builtin_amdgcn_readfirstlane(rt.begin[g]);
-                const int row0 = per * begin + i * count - cur.r0;
-                const TX *const x[1] = {
-                    (const TX *)(now + (row0 + (r < count ? r : count - 1)) * kRowBytes + c * 16)};
-                const int ahead =
-                    j + kDownWaves < cur.units ? cur.u0 + j + kDownWaves : wave < nxt.units ? nxt.u0 + wave : -1;
-                loaded = ahead >= 0;
-                const int next_b0 = loaded ? aim(ahead) : -1;
-                f32x4 part[1][1];
-                mx4_zero(part);
-                stream_compute<WIDE, true>(it, x, part, nb - i * kStreamBlocks, 1, rows, next_b0, nb, c, bad);
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (4 * c + k < count) {
-                        const int tok = rt.pairs[begin + 4 * c + k] / top_k;
-                        out[wave][tok * 16 + r] += part[0][0][k];
-                    }
-                // another lane may add to the same place next time
-                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            }
-            if (!loaded && wave < nxt.units) {         // nothing was left for it in this stage
-                loaded = true;
-                stream_load(it, rows, aim(nxt.u0 + wave), nb, c);
-            }
-            stash(nxt, then);
-            cur = nxt;
-            open(nxt, cur.u0 + cur.units);
-            fetch(nxt);
-            __syncthreads();
-            uint8_t *const t = now;
-            now = then;
-            then = t;
-        }
-    };
-    contract.template operator()<false>();
-    if constexpr (std::is_same<TX, f16>::value)
-        if (__syncthreads_or(bad))                     // scales that fp16 cannot hold
-            contract.template operator()<true>();
-
+    for (int k = lane; k < TOK * 16; k += 64)
+        out[wave][k] = 0.f;
+    const int first = WIDE ? 0 : wave, step = WIDE ? 1 : kWaves;   // of a stage's units, this wave's
+    Stage cur, nxt;
+    act.open(cur, first_unit);
+    act.fetch(cur);
+    StreamItem<1> it;                                  // the wave's next unit, if `loaded`
+    bool loaded = first < cur.units;
+    if (loaded)
+        stream_load(it, rows, aim(first_unit + first), nb, c);
+    act.stash(cur, bufs[0]);
+    act.open(nxt, cur.u0 + cur.units);
+    act.fetch(nxt);
     __syncthreads();
-    for (int k = threadIdx.x; k < M * 16; k += 64 * kDownWaves) {
-        float sum = out[0][k];
+    uint8_t *now = bufs[0], *then = bufs[1];
+#pragma unroll 1
+    while (cur.units) {
+#pragma unroll 1
+        for (int j = first; j < cur.units; j += step) {
+            const int u = cur.u0 + j, g = u / per, i = u - g * per;
+            const int count = rt.size(g), begin = __builtin_amdgcn_readfirstlane(rt.begin[g]);
+            const int row0 = per * begin + i * count - cur.r0;
+            const uint8_t *const row = now + (row0 + (r < count ? r : count - 1)) * kRowBytes + c * 16;
+            const bf16 *const x[2] = {(const bf16 *)row, (const bf16 *)(row + kPartBytes)};
+            const int ahead = j + step < cur.units ? u + step : first < nxt.units ? nxt.u0 + first : -1;
+            loaded = ahead >= 0;
+            const int next_b0 = loaded ? aim(ahead) : -1;
+            f32x4 part[2][1];
+            bool bad;                                  // of fp16 operands only
+            mx4_zero(part);
+            stream_compute<false, true>(it, x, part, nb - i * kStreamBlocks, rows, next_b0, nb, c, bad);
 #pragma unroll
-        for (int w = 1; w < kDownWaves; ++w)
-            sum += out[w][k];
-        const int64_t at = (int64_t)(k >> 4) * hidden + blockIdx.x * 16 + (k & 15);
-        if (gridDim.y > 1)
-            sums[blockIdx.y * (int64_t)M * hidden + at] = sum;
-        else
-            Y[at] = static_cast<TX>(sum);
+            for (int k = 0; k < 4; ++k)
+                if (4 * c + k < count) {
+                    const int tok = rt.pairs[begin + 4 * c + k] / top_k;
+                    out[wave][tok * 16 + r] += part[0][0][k] + part[1][0][k];
+                }
+            // another lane may add to the same place next time
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        }
+        if (!loaded && first < nxt.units) {            // nothing was left for it in this stage
+            loaded = true;
+            stream_load(it, rows, aim(nxt.u0 + first), nb, c);
+        }
+        act.stash(nxt, then);
+        cur = nxt;
+        act.open(nxt, cur.u0 + cur.units);
+        act.fetch(nxt);
+        __syncthreads();
+        uint8_t *const t = now;
+        now = then;
+        then = t;
+    }
+
+    const int64_t part0 = blockIdx.y * (int64_t)M * hidden;
+    if constexpr (WIDE) {
+        if (!idle)
+            for (int k = lane; k < M * 16; k += 64) {
+                const int64_t at = (int64_t)(k >> 4) * hidden + tile * 16 + (k & 15);
+                if (gridDim.y > 1)
+                    sums[part0 + at] = out[wave][k];
+                else
+                    Y[at] = static_cast<TY>(out[wave][k]);
+            }
+    } else {
+        __syncthreads();
+        for (int k = threadIdx.x; k < M * 16; k += 64 * kWaves) {
+            float sum = out[0][k];
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w)
+                sum += out[w][k];
+            const int64_t at = (int64_t)(k >> 4) * hidden + tile * 16 + (k & 15);
+            if (gridDim.y > 1)
+                sums[part0 + at] = sum;
+            else
+                Y[at] = static_cast<TY>(sum);
+        }
     }
 }
 
@@ -490,8 +528,18 @@ __global__ __launch_bounds__(256) void k_mx4_moe_sum(const float *__restrict__ s
     const int i = blockIdx.x * 256 + threadIdx.x;
     if (i >= n)
         return;
-    float v = sums[i];
-    for (int z = 1; z < Z; ++z)
+    float v = 0.f;
+    int z = 0;
+    for (; z + 8 <= Z; z += 8) {                       // eight loads in flight, added in order
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            x[k] = sums[(int64_t)(z + k) * n + i];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            v += x[k];
+    }
+    for (; z < Z; ++z)
         v += sums[(int64_t)z * n + i];
     Y[i] = static_cast<TX>(v);
 }
@@ -504,19 +552,19 @@ void logits(const TX *X, int M, int hidden, const TX *router, int E, float *out,
 
 template <typename TX, int S>
 void up(const TX *X, int pairs, int most, int hidden, int inter, int top_k, const int32_t *ids, const float *weights,
-        const uint8_t *gu, const uint8_t *gus, TX *h, hipStream_t st)
+        const uint8_t *gu, const uint8_t *gus, bf16 *h, hipStream_t st)
 {
     const int tiles = inter / 16, per = kUpWaves / S;
     k_mx4_moe_up<TX, S><<<dim3((tiles + per - 1) / per, most), 64 * kUpWaves, 0, st>>>(X, pairs, hidden, inter, top_k,
                                                                                       ids, weights, gu, gus, h);
 }
 
-template <typename TX, int TOK, int ROWS>
-void down(int Z, const TX *h, int M, int hidden, int inter, int top_k, const int32_t *ids, const uint8_t *dn,
-          const uint8_t *dns, TX *Y, float *sums, hipStream_t st)
+template <typename TY, int TOK, int ROWS, bool WIDE>
+void down(const Mx4DownPlan &plan, const bf16 *h, int M, int hidden, int inter, int top_k, const int32_t *ids,
+          const uint8_t *dn, const uint8_t *dns, TY *Y, float *sums, hipStream_t st)
 {
-    k_mx4_moe_down<TX, TOK, ROWS><<<dim3(hidden / 16, Z), 64 * kDownWaves, 0, st>>>(h, M, hidden, inter, top_k, ids,
-                                                                                   dn, dns, Y, sums);
+    k_mx4_moe_down<TY, TOK, ROWS, WIDE><<<dim3(plan.blocks, plan.parts), 64 * plan.waves, 0, st>>>(
+        h, M, hidden, inter, top_k, ids, dn, dns, Y, sums);
 }
 
 template <typename TX>
@@ -528,7 +576,7 @@ hipError_t moe(const void *X, int M, int hidden, int inter, int E, int top_k, in
     int32_t *const ids = (int32_t *)(ws + lay.ids_off);
     float *const weights = (float *)(ws + lay.w_off), *const lg = (float *)(ws + lay.logits_off);
     float *const sums = (float *)(ws + lay.sums_off);
-    TX *const h = (TX *)(ws + lay.h_off);
+    bf16 *const h = (bf16 *)(ws + lay.h_off);
     const TX *const x = (const TX *)X, *const rw = (const TX *)router;
     const int pairs = M * top_k, most = (pairs < E ? pairs : E) + (M > 16 ? pairs / 16 : 0);   // groups at most
     if (M == 1)
@@ -538,9 +586,12 @@ hipError_t moe(const void *X, int M, int hidden, int inter, int E, int top_k, in
     else
         logits<TX, 8>(x, M, hidden, rw, E, lg, st);
     k_mx4_moe_topk<<<dim3(M), 64, 0, st>>>(lg, E, top_k, renorm, ids, weights);
-    // waves a tile: as few as leave about two blocks a unit
+    // Waves a tile: as few as leave about two blocks a unit, since every block
+    // reads the routing and its tokens first (33 tokens, 48 experts of 1056 x
+    // 1408: S = 1 24 us, 2 28 us); with many columns to a wave half as many each
+    // (8 tokens, 8 experts of 4096 x 14336: 109, 101).
     const int64_t tiles = (int64_t)(inter / 16) * most;
-    if (tiles >= 2048)
+    if (tiles >= 2048 && (tiles < 4096 || hidden < 4096))
         up<TX, 1>(x, pairs, most, hidden, inter, top_k, ids, weights, gu, gus, h, st);
     else if (tiles >= 1536)
         up<TX, 2>(x, pairs, most, hidden, inter, top_k, ids, weights, gu, gus, h, st);
@@ -548,13 +599,16 @@ hipError_t moe(const void *X, int M, int hidden, int inter, int E, int top_k, in
         up<TX, 4>(x, pairs, most, hidden, inter, top_k, ids, weights, gu, gus, h, st);
     else
         up<TX, 8>(x, pairs, most, hidden, inter, top_k, ids, weights, gu, gus, h, st);
-    const int Z = mx4_moe_parts(hidden, inter, most);
-    if (M <= 16)
-        down<TX, 16, 64>(Z, h, M, hidden, inter, top_k, ids, dn, dns, (TX *)Y, sums, st);
+    const Mx4DownPlan plan = mx4_down_plan(M, hidden, inter, most);
+    TX *const y = (TX *)Y;
+    if (!plan.wide)
+        down<TX, 16, 32, false>(plan, h, M, hidden, inter, top_k, ids, dn, dns, y, sums, st);
+    else if (M <= 16)
+        down<TX, 16, 32, true>(plan, h, M, hidden, inter, top_k, ids, dn, dns, y, sums, st);
     else
-        down<TX, kMaxTok, 40>(Z, h, M, hidden, inter, top_k, ids, dn, dns, (TX *)Y, sums, st);
-    if (Z > 1)
-        k_mx4_moe_sum<TX><<<dim3((M * hidden + 255) / 256), 256, 0, st>>>(sums, M * hidden, Z, (TX *)Y);
+        down<TX, kMaxTok, 20, true>(plan, h, M, hidden, inter, top_k, ids, dn, dns, y, sums, st);
+    if (plan.parts > 1)
+        k_mx4_moe_sum<TX><<<dim3((M * hidden + 255) / 256), 256, 0, st>>>(sums, M * hidden, plan.parts, y);
     return hipGetLastError();
 }
 

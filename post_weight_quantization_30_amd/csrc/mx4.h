@@ -270,22 +270,21 @@ __device__ __forceinline__ void stream_load_s(u32x4 (&s)[NT], const StreamRows<N
 template <int NT>
 __device__ __forceinline__ void stream_load(StreamItem<NT> &it, const StreamRows<NT> &rows, int b0, int nb, int c)
 {
+    stream_load_s(it.s, rows, b0, nb);
 #pragma unroll
     for (int u = 0; u < 4; ++u)
         stream_load_w(it.w, u, rows, b0, nb, c);
-    stream_load_s(it.s, rows, b0, nb);
 }
 
 // acc += the item's products; x[mt] is the lane's activation row in LDS at the
-// item's first column, plus 8 c columns. `blocks` of the item exist; `tiles`:
-// which token tiles to multiply (bits). ROLL: the item of `next` at block
-// next_b0 takes its place, load by load as registers are used up (next_b0 < 0:
-// none). One register set then keeps a wave's stream going; with two row tiles
+// item's first column, plus 8 c columns. `blocks` of the item exist. ROLL: the
+// item of `next` at block next_b0 takes its place, load by load as registers are
+// used up (next_b0 < 0: none). One register set then keeps a wave's stream going; with two row tiles
 // a wave, where registers allow it, two sets that change places are faster.
 template <bool WIDE, bool ROLL, typename TX, int MT, int NT>
 __device__ __forceinline__ void stream_compute(StreamItem<NT> &it, const TX *const (&x)[MT], f32x4 (&acc)[MT][NT],
-                                               int blocks, int tiles, const StreamRows<NT> &next, int next_b0, int nb,
-                                               int c, bool &bad)
+                                               int blocks, const StreamRows<NT> &next, int next_b0, int nb, int c,
+                                               bool &bad)
 {
     typedef typename Vec8<TX>::type vec;
     u32x4 sn[NT];
@@ -322,8 +321,6 @@ __device__ __forceinline__ void stream_compute(StreamItem<NT> &it, const TX *con
             }
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-                if (MT > 1 && !(tiles >> mt & 1))
-                    continue;
                 const vec xv = load8(x[mt] + (4 * u + s) * 32);
                 if constexpr (WIDE) {
                     __builtin_amdgcn_sched_barrier(0);

@@ -86,7 +86,7 @@ def test_gemm_a4_refusals(L, kw, status):
     (dict(E=0), -1), (dict(k=0), -1), (dict(k=9), -1), (dict(dtype=3), -1),
     (dict(dtype=0), -5), (dict(M=65), -5), (dict(E=257), -5), (dict(E=20, k=17), -5), (dict(hidden=1 << 21), -5),
     (dict(inter=1 << 21), -5), *[({k: ODD}, -5) for k in ("X", "router", "gu", "dn", "ws")],
-    (dict(ws=None), -2), (dict(ws_bytes=4 * 2 * 96 * 2), -2),
+    (dict(ws=None), -2), (dict(ws_bytes=4 * 2 * 96 * 4), -2),
 ])
 def test_moe_refusals(L, kw, status):
     a = dict(X=FAKE, dtype=2, M=4, hidden=64, inter=96, E=8, k=2, router=FAKE, gu=FAKE, gus=FAKE, dn=FAKE, dns=FAKE,
@@ -98,11 +98,11 @@ def test_moe_refusals(L, kw, status):
 
 def test_moe_workspace_size(L):
     n = awq.mx4_moe_workspace_size(4, 4096, 96, 2)
-    need = 8 * 4 + 8 * 4 + 8 * 96 * 2                  # ids, weights, intermediate
+    need = 8 * 4 + 8 * 4 + 8 * 96 * 4                  # ids, weights, intermediate (two parts)
     need += 4 * 256 * 4                                # logits of up to 256 experts
     assert need <= n < need + 4 * 256
     # few hidden columns: the down product in parts, with fp32 sums of each
-    assert awq.mx4_moe_workspace_size(33, 1056, 1408, 4) >= 33 * 4 * (8 + 1408 * 2) + 33 * 1024 + 3 * 33 * 1056 * 4
+    assert awq.mx4_moe_workspace_size(33, 1056, 1408, 4) >= 33 * 4 * (8 + 1408 * 4) + 33 * 1024 + 3 * 33 * 1056 * 4
     for bad in ((0, 64, 96, 2), (65, 64, 96, 2), (4, 0, 96, 2), (4, 40, 96, 2), (4, 64, 0, 2), (4, 64, 90, 2),
                 (4, 64, 96, 0), (4, 64, 96, 17)):
         assert awq.mx4_moe_workspace_size(*bad) == 0
