@@ -406,10 +406,10 @@ def _ptr(t, name, device=None, dtype=None):
 
 def _mx4_cols(codes, scales, what=""):
     """Columns of an MXFP4 matrix (codes uint8 (..., in / 2), scales uint8 (..., in / 32))."""
-    if codes.dim() < 2 or scales.dim() != codes.dim() or codes.shape[:-1] != scales.shape[:-1] \
-            or codes.shape[-1] * 2 != scales.shape[-1] * MX4_BLOCK:
+    c, s = codes.shape, scales.shape
+    if len(c) < 2 or len(s) != len(c) or c[-1] * 2 != s[-1] * MX4_BLOCK or c[0] != s[0] or c[1:-1] != s[1:-1]:
         raise ValueError(f"{what}codes must be (..., in / 2) and {what}scales (..., in / {MX4_BLOCK})")
-    return codes.shape[-1] * 2
+    return c[-1] * 2
 
 
 def mx4_quantize(W, s=None, codes=None, scales=None):
@@ -420,8 +420,8 @@ def mx4_quantize(W, s=None, codes=None, scales=None):
         raise ValueError(f"W must be (..., in) with in a multiple of {MX4_BLOCK}")
     n_in, dev, rows = shape[-1], W.device, shape[0] if len(shape) == 2 else math.prod(shape[:-1])
     cshape, sshape = (*shape[:-1], n_in // 2), (*shape[:-1], n_in // MX4_BLOCK)
-    codes = torch.empty(cshape, dtype=torch.uint8, device=dev) if codes is None else _need(codes, "codes", cshape)
-    scales = torch.empty(sshape, dtype=torch.uint8, device=dev) if scales is None else _need(scales, "scales", sshape)
+    codes = torch.empty(*cshape, dtype=torch.uint8, device=dev) if codes is None else _need(codes, "codes", cshape)
+    scales = torch.empty(*sshape, dtype=torch.uint8, device=dev) if scales is None else _need(scales, "scales", sshape)
     if s is not None:
         s = _ptr(_need(s, "s", (n_in,)), "s", dev, torch.float32)
     _launch("awq_mx4_quantize", dev, _ptr(W, "W"), _dtype_code(W), rows, n_in, s,
@@ -433,7 +433,7 @@ def mx4_dequantize(codes, scales, dtype=torch.bfloat16, out=None):
     """The values (..., in) that MXFP4 codes and scales stand for, as `dtype`."""
     n_in, dev = _mx4_cols(codes, scales), codes.device
     shape = (*codes.shape[:-1], n_in)
-    out = torch.empty(shape, dtype=dtype, device=dev) if out is None else _need(out, "out", shape)
+    out = torch.empty(*shape, dtype=dtype, device=dev) if out is None else _need(out, "out", shape)
     _launch("awq_mx4_dequantize", dev, _ptr(codes, "codes", None, torch.uint8),
             _ptr(scales, "scales", dev, torch.uint8), math.prod(shape[:-1]), n_in, _ptr(out, "out", dev),
             _dtype_code(out))
@@ -448,7 +448,7 @@ def mx4_gemm(X, codes, scales, y=None, y_f32=False):
         raise ValueError("codes must be (out, in / 2) for X (M, in)")
     out, dev = codes.shape[0], X.device
     ydt = torch.float32 if y_f32 else X.dtype
-    y = torch.empty((M, out), dtype=ydt, device=dev) if y is None else _need(y, "y", (M, out))
+    y = torch.empty(M, out, dtype=ydt, device=dev) if y is None else _need(y, "y", (M, out))
     _launch("awq_mx4_gemm", dev, _ptr(X, "X"), _dtype_code(X), M, n_in, _ptr(codes, "codes", dev, torch.uint8),
             _ptr(scales, "scales", dev, torch.uint8), out, _ptr(y, "y", dev, ydt), _DTYPE[ydt])
     return y
@@ -461,7 +461,7 @@ def mx4_gemm_a4(x_codes, x_scales, codes, scales, dtype=torch.bfloat16, y=None):
     if x_codes.dim() != 2 or codes.dim() != 2 or _mx4_cols(codes, scales) != n_in:
         raise ValueError("x_codes must be (M, in / 2) and codes (out, in / 2)")
     M, out, dev = x_codes.shape[0], codes.shape[0], x_codes.device
-    y = torch.empty((M, out), dtype=dtype, device=dev) if y is None else _need(y, "y", (M, out))
+    y = torch.empty(M, out, dtype=dtype, device=dev) if y is None else _need(y, "y", (M, out))
     _launch("awq_mx4_gemm_a4", dev, _ptr(x_codes, "x_codes", None, torch.uint8),
             _ptr(x_scales, "x_scales", dev, torch.uint8), M, n_in, _ptr(codes, "codes", dev, torch.uint8),
             _ptr(scales, "scales", dev, torch.uint8), out, _ptr(y, "y", dev, dtype), _dtype_code(y))
