@@ -348,8 +348,9 @@ size_t awq_gptq_workspace_size(int64_t out, int64_t in);
  *      several layers' or experts' stacked, or activations.
  * awq_mx4_dequantize: out (rows, in) of `dtype` = the values, rounded to nearest
  * even where `dtype` does not hold them (bf16 and fp32 hold all below 2^128).
- * AWQ_ERR_UNSUPPORTED: W, s, codes or out not 16-byte aligned, a matrix of more
- * than 2^43 values, or `in` above 2^23. */
+ * Outputs must not overlap inputs, here and in the calls below.
+ * AWQ_ERR_UNSUPPORTED: W, s, codes or out not 16-byte aligned, 2^37 values or
+ * more, or `in` above 2^23. */
 #define AWQ_MX4_BLOCK 32
 int awq_mx4_quantize(const void *W, int dtype, int64_t rows, int64_t in, const float *s, uint8_t *codes,
                      uint8_t *scales, void *stream);
@@ -367,7 +368,7 @@ int awq_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows
  * rounding to a 16-bit Y. A row of X or W that holds a NaN makes its own
  * outputs NaN and no others.
  * AWQ_ERR_UNSUPPORTED: x_dtype AWQ_F32, X or codes (xcodes) not 16-byte aligned,
- * M above 2 097 120, or `in` above 2^23. */
+ * M above 2 097 120, out above 2^28, `in` above 2^23, or M * out of 2^38 or more. */
 int awq_mx4_gemm(const void *X, int x_dtype, int64_t M, int64_t in, const uint8_t *codes,
                  const uint8_t *scales, int64_t out, void *Y, int y_dtype, void *stream);
 int awq_mx4_gemm_a4(const uint8_t *xcodes, const uint8_t *xscales, int64_t M, int64_t in,

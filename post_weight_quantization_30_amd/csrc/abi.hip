@@ -454,13 +454,13 @@ int awq_quantize_pack_clip(const void *W, int dtype, int64_t out, int64_t in, co
 
 namespace {
 
-// A matrix (rows, in) of MXFP4 blocks; the launches count chunks of 8 values
-// in blocks of 1024 chunks.
+// A matrix (rows, in) of MXFP4 blocks; a launch has one thread for 32 values and
+// less than 2^32 of them.
 int mx4_shape(int64_t rows, int64_t in)
 {
     if (rows < 1 || in < 1 || in % AWQ_MX4_BLOCK != 0 || rows > INT64_MAX / in)
         return AWQ_ERR_INVALID_ARG;
-    if (rows * in > (int64_t)1 << 43 || in > (int64_t)1 << 23)
+    if (rows * in >= (int64_t)1 << 37 || in > (int64_t)1 << 23)
         return AWQ_ERR_UNSUPPORTED;
     return AWQ_OK;
 }
@@ -470,7 +470,8 @@ int mx4_gemm_shape(int64_t M, int64_t in, int64_t out)
     if (M < 1 || out < 1 || in < 1 || in % AWQ_MX4_BLOCK != 0 || out > INT64_MAX / in || M > INT64_MAX / in ||
         M > INT64_MAX / out)
         return AWQ_ERR_INVALID_ARG;
-    if (M > 65535LL * 32 || in > (int64_t)1 << 23 || (out + 15) / 16 > (int64_t)0x7fffffff)
+    // the kernels' 32-bit offsets within a tile; less than 2^32 threads a launch
+    if (M > 65535LL * 32 || in > (int64_t)1 << 23 || out > (int64_t)1 << 28 || M * out >= (int64_t)1 << 38)
         return AWQ_ERR_UNSUPPORTED;
     return AWQ_OK;
 }

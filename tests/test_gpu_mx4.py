@@ -412,6 +412,20 @@ def test_moe_nan_reaches_only_its_tokens(awq, M):
     assert np.isnan(Y[hit]).all() and np.isfinite(Y[~hit]).all()
 
 
+def test_moe_nan_logits_rank_lowest(awq):
+    """A router row of NaN: its expert is chosen by nobody while others are left."""
+    say("moe nan router")
+    X, X32, R, R32, gu, dn = moe_inputs(21, 7, 96, 64, "f16", 77)
+    gc, gs, gcd, gsd = mx4(awq, gu)
+    dc, ds, dcd, dsd = mx4(awq, dn)
+    R[3] = NAN
+    keep = [0, 1, 2, 4, 5, 6]
+    Y = awq.mx4_moe(X, R, gcd, gsd, dcd, dsd, 3).float().cpu().numpy()
+    refs = [moe_reference(X32, R32[keep], gc[keep], gs[keep], dc[keep], ds[keep], ids, True, "f16")
+            for ids in moe_routings(X32, R32[keep], 3)]
+    assert (np.min([(np.abs(Y - w) / b).max(1) for w, b in refs], axis=0) <= 1).all()
+
+
 def test_moe_refuses_a_short_workspace(awq):
     X, X32, R, R32, gu, dn = moe_inputs(4, 3, 64, 64, "bf16", 2)
     gc, gs, gcd, gsd = mx4(awq, gu)

@@ -35,7 +35,7 @@ def test_declared_and_exported(L):
 @pytest.mark.parametrize("kw,status", [
     (dict(W=None), -1), (dict(codes=None), -1), (dict(scales=None), -1), (dict(dtype=3), -1), (dict(dtype=-1), -1),
     (dict(rows=0), -1), (dict(rows=-4), -1), (dict(n=0), -1), (dict(n=48), -1), (dict(rows=1 << 60), -1),
-    (dict(rows=1 << 40), -5), (dict(rows=1, n=1 << 31), -5),
+    (dict(rows=1 << 40), -5), (dict(rows=1, n=1 << 31), -5), (dict(rows=1 << 31), -5), (dict(rows=1, n=(1 << 23) + 32), -5),
     (dict(W=ODD), -5), (dict(s=ODD), -5), (dict(codes=ODD), -5),
 ])
 def test_quantize_refusals(L, kw, status):
@@ -60,6 +60,7 @@ GEMM_BAD = [
     (dict(M=0), -1), (dict(out=0), -1), (dict(n=0), -1), (dict(n=16), -1), (dict(y=3), -1),
     (dict(M=1 << 60), -1), (dict(out=1 << 60), -1), (dict(M=1 << 32, out=1 << 32), -1),
     (dict(M=65535 * 32 + 1), -5), (dict(n=1 << 31), -5), (dict(out=1 << 36), -5),
+    (dict(n=(1 << 23) + 32), -5), (dict(out=(1 << 28) + 1), -5), (dict(M=1 << 20, out=1 << 18), -5),
     (dict(X=ODD), -5), (dict(codes=ODD), -5),
 ]
 
