@@ -151,11 +151,8 @@ hipError_t quantize(const void *W, int64_t rows, int64_t in, const float *s, uin
         k_mx4_quantize<T><<<dim3((uint32_t)blocks), kThreads, 0, st>>>((const T *)W, chunks, codes, scales);
     } else {
         const int64_t xb = (cpr + kThreads - 1) / kThreads;
-        // rows per block: enough blocks to fill the chip, and within the grid's 65535
-        int64_t rpb = rows * xb / 4096;
-        rpb = rpb < kPer ? kPer : (rpb + kPer - 1) / kPer * kPer;
-        if ((rows + rpb - 1) / rpb > 65535)
-            rpb = (rows + 65534) / 65535;
+        // rows per block: one round of loads, and within the grid's 65535
+        const int64_t rpb = rows <= 65535 * kPer ? kPer : (rows + 65534) / 65535;
         k_mx4_quantize_s<T><<<dim3((uint32_t)xb, (uint32_t)((rows + rpb - 1) / rpb)), kThreads, 0, st>>>(
             (const T *)W, s, rows, cpr, rpb, codes, scales);
     }

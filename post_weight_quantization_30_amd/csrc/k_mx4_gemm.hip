@@ -75,7 +75,7 @@ __global__ __launch_bounds__(512, 4) void k_mx4_gemv(const TX *__restrict__ X, i
     rows.lane((uint32_t)(first + r < out ? r : out - 1 - first), c, nb);
     const int stride = kc * 64 + 16, row = (r < M ? r : M - 1) * stride + c * 16;
     const int items = (nb + kStreamBlocks - 1) / kStreamBlocks, per = kc / kStreamBlocks;
-    bool bad = false;
+    F16Range range;
     f32x4 acc[1][1];
 
     auto stage = [&](int i0) {                             // columns of items i0 ... i0 + per - 1
@@ -102,13 +102,13 @@ __global__ __launch_bounds__(512, 4) void k_mx4_gemv(const TX *__restrict__ X, i
             for (; i < end; i += S) {
                 const TX *const x[1] = {(const TX *)(lds + row + (i - i0) * kStreamBlocks * 64)};
                 stream_compute<WIDE, true>(it, x, acc, nb - i * kStreamBlocks, rows,
-                                     i + S < items ? (i + S) * kStreamBlocks : -1, nb, c, bad);
+                                     i + S < items ? (i + S) * kStreamBlocks : -1, nb, c, range);
             }
         }
     };
     contract.template operator()<false>();
     if constexpr (std::is_same<TX, f16>::value)
-        if (__syncthreads_or(bad))                         // scales that fp16 cannot hold
+        if (__syncthreads_or(range.exceeded()))          // scales that fp16 cannot hold
             contract.template operator()<true>();
     if constexpr (S > 1) {
         f32x4 *const red = reinterpret_cast<f32x4 *>(lds);

@@ -243,7 +243,7 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void k_mx4_moe_up(const TX *__res
     const int count = rt.size(group);
     const int kc = stream_chunk(count, nb), stride = kc * 64 + 16, per = kc / kStreamBlocks;
     const int xrow = (r < count ? r : count - 1) * stride + c * 16;
-    bool bad = false;
+    F16Range range;
     f32x4 acc[1][2];
     auto contract = [&]<bool WIDE>() {
         mx4_zero(acc);
@@ -267,7 +267,7 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void k_mx4_moe_up(const TX *__res
                 if (i + S < items)
                     stream_load(next, rows, (i + S) * kStreamBlocks, nb, c);
                 const TX *const x[1] = {(const TX *)(lds + xrow + (i - i0) * kStreamBlocks * 64)};
-                stream_compute<WIDE, false>(cur, x, acc, nb - i * kStreamBlocks, rows, -1, nb, c, bad);
+                stream_compute<WIDE, false>(cur, x, acc, nb - i * kStreamBlocks, rows, -1, nb, c, range);
                 i += S;
             };
             while (i < end) {
@@ -284,7 +284,7 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void k_mx4_moe_up(const TX *__res
     };
     contract.template operator()<false>();
     if constexpr (std::is_same<TX, f16>::value)
-        if (__syncthreads_or(bad))                 // scales that fp16 cannot hold
+        if (__syncthreads_or(range.exceeded()))          // scales that fp16 cannot hold
             contract.template operator()<true>();
 
     if constexpr (S > 1) {
@@ -469,9 +469,9 @@ __global__ __launch_bounds__(1024) void k_mx4_moe_down(const bf16 *__restrict__ 
             loaded = ahead >= 0;
             const int next_b0 = loaded ? aim(ahead) : -1;
             f32x4 part[2][1];
-            bool bad;                                  // of fp16 operands only
+            F16Range range;                            // of fp16 operands only
             mx4_zero(part);
-            stream_compute<false, true>(it, x, part, nb - i * kStreamBlocks, rows, next_b0, nb, c, bad);
+            stream_compute<false, true>(it, x, part, nb - i * kStreamBlocks, rows, next_b0, nb, c, range);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 if (4 * c + k < count) {

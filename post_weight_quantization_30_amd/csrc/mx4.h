@@ -56,6 +56,20 @@ __device__ __forceinline__ f16x8 mx4_to_f16(uint32_t w, float s)
 // fp16 holds 0.5 * 2^E .. 6 * 2^E as normal numbers for E in [-13, 13].
 __device__ __forceinline__ bool mx4_fits_f16(uint32_t byte) { return byte - 114u <= 26u; }
 
+// Whether all scale bytes seen fit fp16, four at a time: the largest byte - 114
+// as unsigned halves.
+struct F16Range {
+    typedef uint16_t half2 __attribute__((ext_vector_type(2)));
+    half2 worst = {0, 0};
+    __device__ __forceinline__ void see(uint32_t bytes)
+    {
+        const half2 from = {114, 114};
+        worst = __builtin_elementwise_max(worst, __builtin_bit_cast(half2, bytes & 0x00FF00FFu) - from);
+        worst = __builtin_elementwise_max(worst, __builtin_bit_cast(half2, bytes >> 8 & 0x00FF00FFu) - from);
+    }
+    __device__ __forceinline__ bool exceeded() const { return worst[0] > 26 || worst[1] > 26; }
+};
+
 // fp16 values as the exact sum of two bf16 parts (11 significand bits = 8 + 3;
 // an infinity stays in the first part).
 __device__ __forceinline__ void split_f16(const f16x8 &x, bf16x8 &hi, bf16x8 &lo)
@@ -144,12 +158,14 @@ __device__ __forceinline__ void mx4_load(Mx4Item<TX, U> &it, const Mx4Rows<TX> &
 
 // acc += the item's products. WIDE is for fp16 activations under scales that
 // fp16 cannot hold: weights in bf16, activations as two bf16 parts. The plain
-// form reports such scales in `bad`.
+// form notes the scales it meets in `range`.
 template <bool WIDE, typename TX, int U>
-__device__ __forceinline__ void mx4_compute(Mx4Item<TX, U> &it, f32x4 &acc, int b0, int nb, bool &bad)
+__device__ __forceinline__ void mx4_compute(Mx4Item<TX, U> &it, f32x4 &acc, int b0, int nb, F16Range &range)
 {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+        if constexpr (std::is_same<TX, f16>::value && !WIDE)
+            range.see(it.ws[u]);
         transpose4(it.w[u]);
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
@@ -165,7 +181,6 @@ __device__ __forceinline__ void mx4_compute(Mx4Item<TX, U> &it, f32x4 &acc, int 
                 acc = mx4_mfma(lo, w, acc);
             } else if constexpr (std::is_same<TX, f16>::value) {
                 acc = mx4_mfma(it.x[u][s], mx4_to_f16(it.w[u][s], mx4_scale(byte)), acc);
-                bad = bad || !mx4_fits_f16(byte);
             } else {
                 acc = mx4_mfma(it.x[u][s], mx4_to_bf16(it.w[u][s], mx4_scale(byte)), acc);
             }
@@ -184,30 +199,30 @@ __device__ __forceinline__ void mx4_wave(const Mx4Rows<TX> &rows, f32x4 &acc, in
     if (first >= nb)
         return;
     Mx4Item<TX, U> a, b;
-    bool bad = false;
+    F16Range range;
     int i = first;
     mx4_load(a, rows, i, nb, c);
     while (true) {
         if (i + step < nb)
             mx4_load(b, rows, i + step, nb, c);
-        mx4_compute<false>(a, acc, i, nb, bad);
+        mx4_compute<false>(a, acc, i, nb, range);
         i += step;
         if (i >= nb)
             break;
         if (i + step < nb)
             mx4_load(a, rows, i + step, nb, c);
-        mx4_compute<false>(b, acc, i, nb, bad);
+        mx4_compute<false>(b, acc, i, nb, range);
         i += step;
         if (i >= nb)
             break;
     }
     if constexpr (std::is_same<TX, f16>::value) {
-        if (__any(bad)) {
+        if (__any(range.exceeded())) {
             acc = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
             for (i = first; i < nb; i += step) {
                 mx4_load(a, rows, i, nb, c);
-                mx4_compute<true>(a, acc, i, nb, bad);
+                mx4_compute<true>(a, acc, i, nb, range);
             }
         }
     }
@@ -279,12 +294,12 @@ __device__ __forceinline__ void stream_load(StreamItem<NT> &it, const StreamRows
 // acc += the item's products; x[mt] is the lane's activation row in LDS at the
 // item's first column, plus 8 c columns. `blocks` of the item exist. ROLL: the
 // item of `next` at block next_b0 takes its place, load by load as registers are
-// used up (next_b0 < 0: none). One register set then keeps a wave's stream going; with two row tiles
-// a wave, where registers allow it, two sets that change places are faster.
+// used up (next_b0 < 0: none). One register set then keeps a wave's stream
+// going; with two row tiles a wave two sets that change places are faster.
 template <bool WIDE, bool ROLL, typename TX, int MT, int NT>
 __device__ __forceinline__ void stream_compute(StreamItem<NT> &it, const TX *const (&x)[MT], f32x4 (&acc)[MT][NT],
                                                int blocks, const StreamRows<NT> &next, int next_b0, int nb, int c,
-                                               bool &bad)
+                                               F16Range &range)
 {
     typedef typename Vec8<TX>::type vec;
     u32x4 sn[NT];
@@ -298,6 +313,8 @@ __device__ __forceinline__ void stream_compute(StreamItem<NT> &it, const TX *con
         for (int nt = 0; nt < NT; ++nt) {
             wu[nt] = it.w[nt][u];
             transpose4(wu[nt]);
+            if constexpr (std::is_same<TX, f16>::value && !WIDE)
+                range.see(it.s[nt][u]);
         }
         if (ROLL && next_b0 >= 0)
             stream_load_w(it.w, u, next, next_b0, nb, c);
@@ -314,7 +331,6 @@ __device__ __forceinline__ void stream_compute(StreamItem<NT> &it, const TX *con
                     wide[nt] = mx4_to_bf16(wu[nt][s], mx4_scale(byte));
                 } else if constexpr (std::is_same<TX, f16>::value) {
                     w[nt] = mx4_to_f16(wu[nt][s], mx4_scale(byte));
-                    bad = bad || !mx4_fits_f16(byte);
                 } else {
                     w[nt] = mx4_to_bf16(wu[nt][s], mx4_scale(byte));
                 }
