@@ -77,67 +77,95 @@ __global__ __launch_bounds__(256) void k_mx4_moe_logits(const TX *__restrict__ X
         logits[(int64_t)(m0 + t) * E + e] = (part[0][t] + part[1][t]) + (part[2][t] + part[3][t]);
 }
 
-// Larger logits have larger keys; NaN the lowest, -0 ties with +0.
+// Larger logits have larger keys; NaN the lowest, -0 ties with +0, and 0 is below all.
 __device__ __forceinline__ uint32_t ordered(float x)
 {
     const uint32_t u = __builtin_bit_cast(uint32_t, x);
     if ((u & 0x7FFFFFFFu) > 0x7F800000u)
-        return 0;
+        return 1;
     const uint32_t z = (u << 1) == 0 ? 0 : u;
     return z & 0x80000000u ? ~z : z | 0x80000000u;
 }
 
-// One wave per token: an expert's place is the number of those ahead of it.
-__global__ __launch_bounds__(64) void k_mx4_moe_topk(const float *__restrict__ logits, int E, int top_k, int renorm,
-                                                     int32_t *__restrict__ ids, float *__restrict__ weights)
+// The largest x of the wave.
+__device__ __forceinline__ uint32_t wave_max(uint32_t x)
 {
-    __shared__ __align__(16) uint32_t keys[kMaxE];
-    __shared__ float chosen[kMaxK];
-    __shared__ int chosen_id[kMaxK];
-    const int lane = threadIdx.x;
-    const int64_t m = blockIdx.x;
-    float l[kMaxE / 64];
+    auto with = [&](uint32_t o) { x = x > o ? x : o; };
+    with(__builtin_amdgcn_update_dpp(x, x, 0x111, 0xF, 0xF, false));   // lanes 1, 2, 4, 8 below, within rows of 16
+    with(__builtin_amdgcn_update_dpp(x, x, 0x112, 0xF, 0xF, false));
+    with(__builtin_amdgcn_update_dpp(x, x, 0x114, 0xF, 0xF, false));
+    with(__builtin_amdgcn_update_dpp(x, x, 0x118, 0xF, 0xF, false));
+    with(__builtin_amdgcn_update_dpp(x, x, 0x142, 0xA, 0xF, false));   // lane 15 of the row below
+    with(__builtin_amdgcn_update_dpp(x, x, 0x143, 0xC, 0xF, false));   // lane 31
+    return __builtin_amdgcn_readlane(x, 63);
+}
+
+// Routes a token, by one wave: lane k < top_k gets the k-th expert and its
+// weight. Each is the maximum of the keys that are left, found in 6 steps
+// across the lanes: 16 experts of 256 take a microsecond, where counting the
+// experts ahead of each one takes 8.
+__device__ __forceinline__ void choose(const float *logits, int E, int top_k, int renorm, int lane, int &id,
+                                       float &weight)
+{
+    constexpr int Q = kMaxE / 64;
+    float l[Q], logit = 0.f, top = 0.f;
+    uint32_t keys[Q];
 #pragma unroll
-    for (int q = 0; q < kMaxE / 64; ++q) {
-        const int e = 64 * q + lane;
-        l[q] = e < E ? logits[m * E + e] : 0.f;
-        keys[e] = e < E ? ordered(l[q]) : 0;           // past the last expert: ahead of nobody
-    }
-    __syncthreads();
+    for (int q = 0; q < Q; ++q)
+        l[q] = 64 * q + lane < E ? logits[64 * q + lane] : 0.f;
 #pragma unroll
-    for (int q = 0; q < kMaxE / 64; ++q) {
-        const int e = 64 * q + lane;
-        if (e < E) {
-            const uint32_t key = keys[e];
-            int rank = 0;
-            for (int j = 0; j < E; j += 4) {
-                const u32x4 k4 = *reinterpret_cast<const u32x4 *>(&keys[j]);
+    for (int q = 0; q < Q; ++q)
+        keys[q] = 64 * q + lane < E ? ordered(l[q]) : 0;
+    for (int k = 0; k < top_k; ++k) {
+        uint32_t best = keys[0];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    rank += k4[i] > key || (k4[i] == key && j + i < e) ? 1 : 0;
-            }
-            if (rank < top_k) {
-                chosen[rank] = l[q];
-                chosen_id[rank] = e;
-            }
+        for (int q = 1; q < Q; ++q)
+            best = best > keys[q] ? best : keys[q];
+        best = wave_max(best);
+        int e = 0;
+#pragma unroll
+        for (int q = Q - 1; q >= 0; --q) {             // of equals the lowest
+            const uint64_t at = __ballot(keys[q] == best);
+            e = at ? 64 * q + __builtin_ctzll(at) : e;
         }
+        float v = 0.f;
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+            if (e >> 6 == q) {
+                v = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, l[q]), e & 63));
+                keys[q] = lane == (e & 63) ? 0 : keys[q];
+            }
+        top = k == 0 ? v : top;
+        logit = lane == k ? v : logit;
+        id = lane == k ? e : id;
     }
-    __syncthreads();
-    const float top = chosen[0];
+    const float own = expf(logit - top);
     float total = 0.f;
     if (renorm) {
         for (int k = 0; k < top_k; ++k)
-            total += expf(chosen[k] - top);
+            total += __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, own), k));
     } else {
 #pragma unroll
-        for (int q = 0; q < kMaxE / 64; ++q)
+        for (int q = 0; q < Q; ++q)
             total += 64 * q + lane < E ? expf(l[q] - top) : 0.f;
         for (int off = 32; off > 0; off >>= 1)
             total += __shfl_xor(total, off);
     }
+    weight = own / total;
+}
+
+// A wave per token.
+__global__ __launch_bounds__(64) void k_mx4_moe_topk(const float *__restrict__ logits, int E, int top_k, int renorm,
+                                                     int32_t *__restrict__ ids, float *__restrict__ weights)
+{
+    const int lane = threadIdx.x;
+    const int64_t m = blockIdx.x;
+    int id = 0;
+    float weight;
+    choose(logits + m * E, E, top_k, renorm, lane, id, weight);
     if (lane < top_k) {
-        ids[m * top_k + lane] = chosen_id[lane];
-        weights[m * top_k + lane] = expf(chosen[lane] - top) / total;
+        ids[m * top_k + lane] = id;
+        weights[m * top_k + lane] = weight;
     }
 }
 
@@ -211,13 +239,15 @@ __device__ __forceinline__ void read_routing(Routed &rt, const int32_t *ids, int
 // Block: a group's tokens, 8 / S tiles of 16 columns of its expert's
 // intermediate (16 gate rows and 16 up rows each), S waves a tile splitting the
 // hidden columns. The tokens' activations lie in LDS by chunks of kc blocks;
-// every wave streams its weights (see StreamItem).
+// every wave streams its weights (see StreamItem). ROUTE: every block routes all
+// tokens, a wave each, from the logits, and the first leaves `ids` for `down`.
 constexpr int kUpWaves = 8;
 
-template <typename TX, int S>
+template <typename TX, int S, bool ROUTE>
 __global__ __launch_bounds__(64 * kUpWaves, 4) void k_mx4_moe_up(const TX *__restrict__ X, int pairs, int hidden,
                                                                  int inter, int top_k,
-                                                                 const int32_t *__restrict__ ids,
+                                                                 const float *__restrict__ logits, int E, int renorm,
+                                                                 int32_t *__restrict__ ids,
                                                                  const float *__restrict__ weights,
                                                                  const uint8_t *__restrict__ codes,
                                                                  const uint8_t *__restrict__ scales,
@@ -225,8 +255,26 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void k_mx4_moe_up(const TX *__res
 {
     __shared__ Routed rt;
     __shared__ __align__(16) uint8_t lds[kStreamLds + 16 * 16];
+    __shared__ int32_t own_ids[ROUTE ? kUpWaves * kMaxK : 1];
+    __shared__ float own_weights[ROUTE ? kUpWaves * kMaxK : 1];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    read_routing(rt, ids, pairs, top_k);
+    if constexpr (ROUTE) {
+        if (wave * top_k < pairs) {
+            int id = 0;
+            float weight;
+            choose(logits + wave * E, E, top_k, renorm, lane, id, weight);
+            if (lane < top_k) {
+                own_ids[wave * top_k + lane] = id;
+                own_weights[wave * top_k + lane] = weight;
+                if (blockIdx.x == 0 && blockIdx.y == 0)
+                    ids[wave * top_k + lane] = id;
+            }
+        }
+        __syncthreads();
+        read_routing(rt, own_ids, pairs, top_k);
+    } else {
+        read_routing(rt, ids, pairs, top_k);
+    }
     const int group = (int)blockIdx.y;
     if (group >= rt.groups)
         return;                    // fewer groups than blocks: the whole block leaves
@@ -307,7 +355,7 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void k_mx4_moe_up(const TX *__res
             if (4 * c + k < count) {
                 const int pair = list[4 * c + k];
                 const float gate = acc[0][0][k], up = acc[0][1][k];
-                const float v = gate / (1.0f + expf(-gate)) * up * weights[pair];
+                const float v = gate / (1.0f + expf(-gate)) * up * (ROUTE ? own_weights : weights)[pair];
                 // two bf16 parts: 16 significant bits (an infinity stays in the first)
                 const float hi = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, v) & 0xFFFF0000u);
                 bf16 *const out = h + (int64_t)pair * 2 * inter + col0 + r;
@@ -550,13 +598,13 @@ void logits(const TX *X, int M, int hidden, const TX *router, int E, float *out,
     k_mx4_moe_logits<TX, TOK><<<dim3(E, (M + TOK - 1) / TOK), 256, 0, st>>>(X, M, hidden, router, E, out);
 }
 
-template <typename TX, int S>
-void up(const TX *X, int pairs, int most, int hidden, int inter, int top_k, const int32_t *ids, const float *weights,
-        const uint8_t *gu, const uint8_t *gus, bf16 *h, hipStream_t st)
+template <typename TX, int S, bool ROUTE = false>
+void up(const TX *X, int pairs, int most, int hidden, int inter, int top_k, const float *logits, int E, int renorm,
+        int32_t *ids, const float *weights, const uint8_t *gu, const uint8_t *gus, bf16 *h, hipStream_t st)
 {
     const int tiles = inter / 16, per = kUpWaves / S;
-    k_mx4_moe_up<TX, S><<<dim3((tiles + per - 1) / per, most), 64 * kUpWaves, 0, st>>>(X, pairs, hidden, inter, top_k,
-                                                                                      ids, weights, gu, gus, h);
+    k_mx4_moe_up<TX, S, ROUTE><<<dim3((tiles + per - 1) / per, most), 64 * kUpWaves, 0, st>>>(
+        X, pairs, hidden, inter, top_k, logits, E, renorm, ids, weights, gu, gus, h);
 }
 
 template <typename TY, int TOK, int ROWS, bool WIDE>
@@ -585,20 +633,20 @@ hipError_t moe(const void *X, int M, int hidden, int inter, int E, int top_k, in
         logits<TX, 4>(x, M, hidden, rw, E, lg, st);
     else
         logits<TX, 8>(x, M, hidden, rw, E, lg, st);
-    k_mx4_moe_topk<<<dim3(M), 64, 0, st>>>(lg, E, top_k, renorm, ids, weights);
     // Waves a tile: as few as leave about two blocks a unit, since every block
     // reads the routing and its tokens first (33 tokens, 48 experts of 1056 x
     // 1408: S = 1 24 us, 2 28 us); with many columns to a wave half as many each
     // (8 tokens, 8 experts of 4096 x 14336: 109, 101).
     const int64_t tiles = (int64_t)(inter / 16) * most;
-    if (tiles >= 2048 && (tiles < 4096 || hidden < 4096))
-        up<TX, 1>(x, pairs, most, hidden, inter, top_k, ids, weights, gu, gus, h, st);
-    else if (tiles >= 1536)
-        up<TX, 2>(x, pairs, most, hidden, inter, top_k, ids, weights, gu, gus, h, st);
-    else if (tiles >= 768)
-        up<TX, 4>(x, pairs, most, hidden, inter, top_k, ids, weights, gu, gus, h, st);
-    else
-        up<TX, 8>(x, pairs, most, hidden, inter, top_k, ids, weights, gu, gus, h, st);
+    const int S = tiles >= 2048 && (tiles < 4096 || hidden < 4096) ? 1 : tiles >= 1536 ? 2 : tiles >= 768 ? 4 : 8;
+    // With a wave for every token and blocks for about one round (S = 8), a launch
+    // less: the blocks route for themselves.
+    const bool route = S == 8 && M <= kUpWaves;
+    if (!route)
+        k_mx4_moe_topk<<<dim3(M), 64, 0, st>>>(lg, E, top_k, renorm, ids, weights);
+    auto *const launch_up = S == 1 ? up<TX, 1> : S == 2 ? up<TX, 2> : S == 4 ? up<TX, 4>
+                                 : route ? up<TX, 8, true> : up<TX, 8>;
+    launch_up(x, pairs, most, hidden, inter, top_k, lg, E, renorm, ids, weights, gu, gus, h, st);
     const Mx4DownPlan plan = mx4_down_plan(M, hidden, inter, most);
     TX *const y = (TX *)Y;
     if (!plan.wide)
