@@ -101,43 +101,48 @@ __global__ __launch_bounds__(kThreads) void k_mx4_quantize_s(const T *__restrict
     }
 }
 
-template <typename T> __device__ __forceinline__ void store8(T *p, uint32_t w, float s);
-template <> __device__ __forceinline__ void store8<bf16>(bf16 *p, uint32_t w, float s)
-{
-    *reinterpret_cast<bf16x8 *>(p) = mx4_to_bf16(w, s);
-}
-template <> __device__ __forceinline__ void store8<f16>(f16 *p, uint32_t w, float s)
-{
-    *reinterpret_cast<f16x8 *>(p) = mx4_to_f16(w, s);
-}
-template <> __device__ __forceinline__ void store8<float>(float *p, uint32_t w, float s)
-{
-    const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 0);
-    const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 1);
-    const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 2);
-    const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 3);
-    *reinterpret_cast<f32x4 *>(p) = f32x4{a[0], a[1], b[0], b[1]};
-    *reinterpret_cast<f32x4 *>(p + 4) = f32x4{c[0], c[1], d[0], d[1]};
-}
+// Values a thread makes of one load of codes: 16 bytes of them.
+template <typename T> struct Piece {
+    typedef uint32_t word;
+    static __device__ __forceinline__ typename Vec8<T>::type make(word w, float s)
+    {
+        if constexpr (std::is_same<T, f16>::value)
+            return mx4_to_f16(w, s);
+        else
+            return mx4_to_bf16(w, s);
+    }
+};
+template <> struct Piece<float> {
+    typedef uint16_t word;
+    static __device__ __forceinline__ f32x4 make(word w, float s)
+    {
+        const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4((uint32_t)w, s, 0);
+        const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4((uint32_t)w, s, 1);
+        return f32x4{a[0], a[1], b[0], b[1]};
+    }
+};
 
 template <typename T>
-__global__ __launch_bounds__(kThreads) void k_mx4_dequantize(const uint32_t *__restrict__ codes,
-                                                             const uint8_t *__restrict__ scales, int64_t chunks,
+__global__ __launch_bounds__(kThreads) void k_mx4_dequantize(const typename Piece<T>::word *__restrict__ codes,
+                                                             const uint8_t *__restrict__ scales, int64_t pieces,
                                                              T *__restrict__ out)
 {
-    const int64_t first = (int64_t)blockIdx.x * (kThreads * kPer) + threadIdx.x;
-    uint32_t w[kPer], b[kPer];
+    constexpr int V = 16 / sizeof(T), kEach = 32 / V;  // kEach: 32 values a thread
+    typedef decltype(Piece<T>::make(0, 0.f)) vec;
+    const int64_t first = (int64_t)blockIdx.x * (kThreads * kEach) + threadIdx.x;
+    typename Piece<T>::word w[kEach];
+    uint8_t b[kEach];
 #pragma unroll
-    for (int p = 0; p < kPer; ++p) {
-        const int64_t ch = first + p * kThreads < chunks ? first + p * kThreads : chunks - 1;
-        w[p] = codes[ch];
-        b[p] = scales[ch >> 2];
+    for (int p = 0; p < kEach; ++p) {
+        const int64_t at = first + p * kThreads < pieces ? first + p * kThreads : pieces - 1;
+        w[p] = codes[at];
+        b[p] = scales[at / (32 / V)];
     }
 #pragma unroll
-    for (int p = 0; p < kPer; ++p) {
-        const int64_t ch = first + p * kThreads;
-        if (ch < chunks)
-            store8<T>(out + ch * 8, w[p], mx4_scale(b[p]));
+    for (int p = 0; p < kEach; ++p) {
+        const int64_t at = first + p * kThreads;
+        if (at < pieces)
+            reinterpret_cast<vec *>(out)[at] = Piece<T>::make(w[p], mx4_scale(b[p]));
     }
 }
 
@@ -174,14 +179,19 @@ hipError_t launch_mx4_quantize(const void *W, int dtype, int64_t rows, int64_t i
 hipError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t in, void *out,
                                  int dtype, hipStream_t st)
 {
-    const int64_t chunks = rows * (in / 8), blocks = (chunks + kThreads * kPer - 1) / (kThreads * kPer);
-    const uint32_t *c = (const uint32_t *)codes;
+    auto run = [&](auto *to) {
+        typedef typename std::remove_pointer<decltype(to)>::type T;
+        typedef typename Piece<T>::word word;
+        const int64_t values = rows * in;
+        k_mx4_dequantize<T><<<dim3((uint32_t)((values + kThreads * 32 - 1) / (kThreads * 32))), kThreads, 0, st>>>(
+            (const word *)codes, scales, values / (int64_t)(16 / sizeof(T)), to);
+    };
     if (dtype == AWQ_F32)
-        k_mx4_dequantize<float><<<dim3((uint32_t)blocks), kThreads, 0, st>>>(c, scales, chunks, (float *)out);
+        run((float *)out);
     else if (dtype == AWQ_F16)
-        k_mx4_dequantize<f16><<<dim3((uint32_t)blocks), kThreads, 0, st>>>(c, scales, chunks, (f16 *)out);
+        run((f16 *)out);
     else
-        k_mx4_dequantize<bf16><<<dim3((uint32_t)blocks), kThreads, 0, st>>>(c, scales, chunks, (bf16 *)out);
+        run((bf16 *)out);
     return hipGetLastError();
 }
 

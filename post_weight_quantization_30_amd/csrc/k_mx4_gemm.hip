@@ -420,11 +420,14 @@ __global__ __launch_bounds__(256, 2) void k_mx4_gemm_tile(const TX *__restrict__
     store_tiles<TY, MT>(Y, acc, reinterpret_cast<float *>(lx) + 2048 * wave, m0, n0 + 64 * wave, M, out, lane);
 }
 
-// The sums of four groups of two waves (32 rows each), (0 + 2) + (1 + 3), to Y.
-template <typename TY, int MT>
-__device__ __forceinline__ void add_groups(float (&red)[2][32 * MT][64], f32x16 (&acc)[MT], int group, int wn, int r,
-                                           int h, TY *__restrict__ Y, int64_t m0, int64_t n0, int64_t M, int64_t out)
+// The sums of G groups of 8 / G waves (32 rows each) to Y, added in a fixed
+// order: the upper half of the groups to the lower, until two are left.
+template <int G, typename TY, int MT>
+__device__ __forceinline__ void add_groups(float (&red)[G / 2][32 * MT][256 / G], f32x16 (&acc)[MT], int group, int wn,
+                                           int r, int h, TY *__restrict__ Y, int64_t m0, int64_t n0, int64_t M,
+                                           int64_t out)
 {
+    constexpr int BN = 256 / G;
     auto put = [&](int g) {
 #pragma unroll
         for (int a = 0; a < MT; ++a)
@@ -432,23 +435,26 @@ __device__ __forceinline__ void add_groups(float (&red)[2][32 * MT][64], f32x16 
             for (int i = 0; i < 16; ++i)
                 red[g][32 * a + 8 * (i / 4) + 4 * h + i % 4][32 * wn + r] = acc[a][i];
     };
-    if (group >= 2)
-        put(group - 2);
-    __syncthreads();
-    if (group < 2)
 #pragma unroll
-        for (int a = 0; a < MT; ++a)
+    for (int n = G / 2; n >= 2; n /= 2) {
+        if (group >= n && group < 2 * n)
+            put(group - n);
+        __syncthreads();
+        if (group < n)
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                acc[a][i] += red[group][32 * a + 8 * (i / 4) + 4 * h + i % 4][32 * wn + r];
-    __syncthreads();
+            for (int a = 0; a < MT; ++a)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    acc[a][i] += red[group][32 * a + 8 * (i / 4) + 4 * h + i % 4][32 * wn + r];
+        __syncthreads();
+    }
     if (group < 2)
         put(group);
     __syncthreads();
-    const int n = threadIdx.x & 63;
+    const int n = threadIdx.x % BN;
 #pragma unroll
-    for (int i = 0; i < 4 * MT; ++i) {
-        const int m = (threadIdx.x >> 6) + 8 * i;
+    for (int i = 0; i < 32 * MT * BN / 512; ++i) {
+        const int m = threadIdx.x / BN + 512 / BN * i;
         const float sum = red[0][m][n] + red[1][m][n];
         if (m0 + m < M && n0 + n < out)
             Y[(m0 + m) * out + n0 + n] = static_cast<TY>(sum);
@@ -456,24 +462,24 @@ __device__ __forceinline__ void add_groups(float (&red)[2][32 * MT][64], f32x16 
 }
 
 // 16-bit activations, too few 128 x 256 tiles for the chip. Block: 32 MT tokens
-// x 64 rows, 8 waves: two of 32 rows each in four groups. A round is 256
-// columns, of which each group takes 64; the groups' sums meet in LDS. Such
-// shapes leave one block or two on a unit, so a round's loads go out two rounds
-// ahead; one LDS buffer then does, and leaves room for the second block.
-template <typename TX, typename TY, int MT>
-__global__ __launch_bounds__(512, 4) void k_mx4_gemm_mid(const TX *__restrict__ X, int64_t M, int nb,
+// x 256 / G rows, 8 waves: G groups of 32 rows a wave. A round is 64 G columns,
+// of which each group takes 64; the groups' sums meet in LDS. Such shapes leave
+// one block or two on a unit, so a round's loads go out two rounds ahead. BUF
+// LDS buffers: two need one barrier a round, one leaves room for a second block.
+template <typename TX, typename TY, int MT, int G, int BUF>
+__global__ __launch_bounds__(512, BUF == 2 && MT * G == 8 ? 2 : 4) void k_mx4_gemm_mid(const TX *__restrict__ X, int64_t M, int nb,
                                                          const uint8_t *__restrict__ codes,
                                                          const uint8_t *__restrict__ scales, int64_t out,
                                                          TY *__restrict__ Y)
 {
     typedef typename Vec8<TX>::type vec;
-    constexpr int BM = 32 * MT, BN = 64, G = 4;
-    constexpr int CX = BM * 8 / 128;                   // activation chunks a thread moves in a round
+    constexpr int BM = 32 * MT, BN = 256 / G, GT = 512 / G;     // GT: threads of a group
+    constexpr int CX = BM * 8 / GT;                    // activation chunks a thread moves in a round
     union Lds {
         struct {
-            u32x4 x[G][BM * 8], w[BN * 8];
-            u32x2 ws[BN];
-        } in;
+            u32x4 x[G][BM * 8], w[G / 4][BN * 8];     // of a weight row 8 chunks each
+            u32x2 ws[G / 4][BN];
+        } in[BUF];
         float red[G / 2][BM][BN];
     };
     __shared__ __align__(16) Lds lds;
@@ -484,25 +490,27 @@ __global__ __launch_bounds__(512, 4) void k_mx4_gemm_mid(const TX *__restrict__ 
     m0 *= BM;
     n0 *= BN;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int r = lane & 31, h = lane >> 5, group = wave >> 1, wn = wave & 1;
+    const int r = lane & 31, h = lane >> 5, group = wave / (8 / G), wn = wave % (8 / G);
     const int xrow = nb * 64;                          // bytes of an activation row
-    const int rounds = (nb + 7) / 8;
+    const int rounds = (nb + 2 * G - 1) / (2 * G);
 
     // addresses and row ends as in k_mx4_gemm_tile
     const uint8_t *const xbase = (const uint8_t *)X + m0 * xrow;
     const uint8_t *const wbase = codes + n0 * nb * 16, *const wsbase = scales + n0 * nb;
     const uint32_t mlast = (uint32_t)(M - 1 - m0 < BM - 1 ? M - 1 - m0 : BM - 1);
     const uint32_t nlast = (uint32_t)(out - 1 - n0 < BN - 1 ? out - 1 - n0 : BN - 1);
-    const int q = threadIdx.x & 7, xrow0 = (threadIdx.x & 127) >> 3;
-    const uint32_t wrow = threadIdx.x >> 3;
+    const int q = threadIdx.x & 7, xrow0 = threadIdx.x % GT >> 3;
+    const int wq = threadIdx.x % (2 * G);              // chunk of weight row wrow
+    const uint32_t wrow = threadIdx.x / (2 * G), wsrow = threadIdx.x % BN;
+    const int wshalf = threadIdx.x / BN;               // below G / 4: eight scales of row wsrow
     uint32_t xo[CX];
 #pragma unroll
     for (int i = 0; i < CX; ++i) {
-        const uint32_t row = xrow0 + 16 * i;
+        const uint32_t row = xrow0 + GT / 8 * i;
         xo[i] = (row < mlast ? row : mlast) * (uint32_t)xrow + q * 16;
     }
-    const uint32_t wo = (wrow < nlast ? wrow : nlast) * (uint32_t)nb * 16 + q * 16;
-    const uint32_t wso = (threadIdx.x < nlast ? threadIdx.x : nlast) * (uint32_t)nb;
+    const uint32_t wo = (wrow < nlast ? wrow : nlast) * (uint32_t)nb * 16 + wq * 16;
+    const uint32_t wso = (wsrow < nlast ? wsrow : nlast) * (uint32_t)nb;
 
     f32x16 acc[MT];
     struct Round {
@@ -514,38 +522,44 @@ __global__ __launch_bounds__(512, 4) void k_mx4_gemm_mid(const TX *__restrict__ 
     auto fetch = [&](Round &to, int j) {
         if (j >= rounds)
             return;
-        const int xb = 8 * j + 2 * group + (q >> 2), xover = (xb - (nb - 1)) * 64;     // its block of the row
-        const int wover = (8 * j + q - (nb - 1)) * 16;
-        const uint8_t *const px = xbase + (int64_t)j * 512 + group * 128, *const pw = wbase + (int64_t)j * 128;
+        const int b0 = 2 * G * j, xb = b0 + 2 * group + (q >> 2), xover = (xb - (nb - 1)) * 64;     // its block of the row
+        const int wover = (b0 + wq - (nb - 1)) * 16;
+        const uint8_t *const px = xbase + (int64_t)b0 * 64 + group * 128, *const pw = wbase + (int64_t)b0 * 16;
 #pragma unroll
         for (int i = 0; i < CX; ++i)
             to.x[i] = *reinterpret_cast<const u32x4 *>(px + ((int64_t)xo[i] - (xover > 0 ? xover : 0)));
         to.w = *reinterpret_cast<const u32x4 *>(pw + ((int64_t)wo - (wover > 0 ? wover : 0)));
-        if (threadIdx.x < BN)
-            to.ws = load_scales8(wsbase + wso, 8 * j, nb);
+        if (wshalf < G / 4)
+            to.ws = load_scales8(wsbase + wso, b0 + 8 * wshalf, nb);
     };
     auto stash = [&](Round &from, int j) {
-        if (8 * j + 2 * group + (q >> 2) >= nb)
+        if (j >= rounds)
+            return;
+        auto &in = lds.in[j % BUF];
+        if (2 * G * j + 2 * group + (q >> 2) >= nb)
 #pragma unroll
             for (int i = 0; i < CX; ++i)
                 from.x[i] = u32x4{0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < CX; ++i)
-            lds.in.x[group][swizzled(xrow0 + 16 * i, q)] = from.x[i];
-        lds.in.w[swizzled(wrow, q)] = from.w;
-        if (threadIdx.x < BN)
-            lds.in.ws[threadIdx.x] = from.ws;
+            in.x[group][swizzled(xrow0 + GT / 8 * i, q)] = from.x[i];
+        in.w[wq >> 3][swizzled(wrow, wq & 7)] = from.w;
+        if (wshalf < G / 4)
+            in.ws[wshalf][wsrow] = from.ws;
     };
     auto contract = [&]<bool WIDE>() {
 #pragma unroll
         for (int a = 0; a < MT; ++a)
             acc[a] = f32x16{};
-        auto round = [&](Round &now, int j) {
-            stash(now, j);
-            __syncthreads();
-            fetch(now, j + 2);
-            const u32x4 w = lds.in.w[swizzled(32 * wn + r, 2 * group + h)];
-            const u32x2 ws = lds.in.ws[32 * wn + r];
+        auto round = [&](Round &next, int j) {         // next: round j + 1 (one buffer: j)
+            if constexpr (BUF == 1) {
+                stash(next, j);
+                __syncthreads();
+                fetch(next, j + 2);
+            }
+            auto &in = lds.in[j % BUF];
+            const u32x4 w = in.w[group >> 2][swizzled(32 * wn + r, 2 * (group & 3) + h)];
+            const u32x2 ws = in.ws[group >> 2][32 * wn + r];
             const uint32_t byte = (group & 2 ? ws[1] : ws[0]) >> (16 * (group & 1) + 8 * h) & 0xFFu;
             if constexpr (std::is_same<TX, f16>::value && !WIDE)
                 bad = bad || !mx4_fits_f16(byte);
@@ -561,7 +575,7 @@ __global__ __launch_bounds__(512, 4) void k_mx4_gemm_mid(const TX *__restrict__ 
                     wv = mx4_to_bf16(w[s], mx4_scale(byte));
 #pragma unroll
                 for (int a = 0; a < MT; ++a) {
-                    const u32x4 x = lds.in.x[group][swizzled(32 * a + r, 4 * h + s)];
+                    const u32x4 x = in.x[group][swizzled(32 * a + r, 4 * h + s)];
                     if constexpr (WIDE) {
                         bf16x8 hi, lo;
                         split_f16(__builtin_bit_cast(f16x8, x), hi, lo);
@@ -572,14 +586,23 @@ __global__ __launch_bounds__(512, 4) void k_mx4_gemm_mid(const TX *__restrict__ 
                     }
                 }
             }
+            if constexpr (BUF == 2) {
+                stash(next, j + 1);
+                fetch(next, j + 3);
+            }
             __syncthreads();
         };
         fetch(even, 0);
         fetch(odd, 1);
+        if constexpr (BUF == 2) {
+            stash(even, 0);
+            fetch(even, 2);
+            __syncthreads();
+        }
         for (int j = 0; j < rounds; j += 2) {
-            round(even, j);
+            round(BUF == 2 ? odd : even, j);
             if (j + 1 < rounds)
-                round(odd, j + 1);
+                round(BUF == 2 ? even : odd, j + 1);
         }
     };
     contract.template operator()<false>();
@@ -587,7 +610,7 @@ __global__ __launch_bounds__(512, 4) void k_mx4_gemm_mid(const TX *__restrict__ 
         if (__syncthreads_or(bad))                     // scales that fp16 cannot hold
             contract.template operator()<true>();
 
-    add_groups<TY, MT>(lds.red, acc, group, wn, r, h, Y, m0, n0, M, out);
+    add_groups<G, TY, MT>(lds.red, acc, group, wn, r, h, Y, m0, n0, M, out);
 }
 
 // The scale bytes h, h + 2, h + 4, h + 6 of eight: those of lane (r, h)'s blocks
@@ -748,16 +771,17 @@ __global__ __launch_bounds__(512, 2) void k_mx4_gemm_tile4(const uint8_t *__rest
 }
 
 // MXFP4 activations, too few 256 x 256 tiles for the chip, or few tokens. Block:
-// 32 MT tokens x 64 rows, 8 waves: two of 32 rows each in four groups. A round
-// is 1024 columns, of which each group takes 256; the groups' sums meet in LDS.
-template <typename TY, int MT>
+// 32 MT tokens x 256 / G rows, 8 waves: G groups of 32 rows a wave. A round is
+// 256 G columns, of which each group takes 256; the groups' sums meet in LDS.
+template <typename TY, int MT, int G>
 __global__ __launch_bounds__(512, 4) void k_mx4_gemm_mid4(const uint8_t *__restrict__ xcodes,
                                                           const uint8_t *__restrict__ xscales, int64_t M, int nb,
                                                           const uint8_t *__restrict__ codes,
                                                           const uint8_t *__restrict__ scales, int64_t out,
                                                           TY *__restrict__ Y)
 {
-    constexpr int BM = 32 * MT, BN = 64, G = 4, CX = BM / 16, CW = BN / 16;
+    constexpr int BM = 32 * MT, BN = 256 / G, GT = 512 / G, CX = BM * 8 / GT, CW = BN * 8 / GT;
+    static_assert(BM + BN <= GT);                      // a thread moves one row's scales
     union Lds {
         struct {
             u32x4 x[G][BM * 8], w[G][BN * 8];
@@ -773,24 +797,24 @@ __global__ __launch_bounds__(512, 4) void k_mx4_gemm_mid4(const uint8_t *__restr
     m0 *= BM;
     n0 *= BN;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int r = lane & 31, h = lane >> 5, group = wave >> 1, wn = wave & 1;
-    const int rounds = (nb + 31) / 32;
+    const int r = lane & 31, h = lane >> 5, group = wave / (8 / G), wn = wave % (8 / G);
+    const int rounds = (nb + 8 * G - 1) / (8 * G);
 
-    // addresses as in k_mx4_gemm_tile; a group's 128 threads move its columns
+    // addresses as in k_mx4_gemm_tile; a group's threads move its columns
     const uint8_t *const xbase = xcodes + m0 * nb * 16, *const xsbase = xscales + m0 * nb;
     const uint8_t *const wbase = codes + n0 * nb * 16, *const wsbase = scales + n0 * nb;
     const uint32_t mlast = (uint32_t)(M - 1 - m0 < BM - 1 ? M - 1 - m0 : BM - 1);
     const uint32_t nlast = (uint32_t)(out - 1 - n0 < BN - 1 ? out - 1 - n0 : BN - 1);
-    const int gt = threadIdx.x & 127, q = gt & 7, row0 = gt >> 3;      // chunk q of rows row0 + 16 i
+    const int gt = threadIdx.x % GT, q = gt & 7, row0 = gt >> 3;       // chunk q of rows row0 + GT / 8 i
     uint32_t xo[CX], wo[CW];
 #pragma unroll
     for (int i = 0; i < CX; ++i) {
-        const uint32_t row = row0 + 16 * i;
+        const uint32_t row = row0 + GT / 8 * i;
         xo[i] = (row < mlast ? row : mlast) * (uint32_t)nb * 16 + q * 16;
     }
 #pragma unroll
     for (int i = 0; i < CW; ++i) {
-        const uint32_t row = row0 + 16 * i;
+        const uint32_t row = row0 + GT / 8 * i;
         wo[i] = (row < nlast ? row : nlast) * (uint32_t)nb * 16 + q * 16;
     }
     // scales: the group's first BN threads a weight row each, the others an activation row
@@ -804,7 +828,7 @@ __global__ __launch_bounds__(512, 4) void k_mx4_gemm_mid4(const uint8_t *__restr
     u32x4 xr[CX], wr[CW];
     u32x2 sr;
     auto fetch = [&](int j) {                          // zeros, under scale 1, past a row's end
-        const int b0 = 32 * j + 8 * group;             // the group's first block
+        const int b0 = 8 * G * j + 8 * group;             // the group's first block
         const uint8_t *const px = xbase + (int64_t)b0 * 16, *const pw = wbase + (int64_t)b0 * 16;
         if (b0 + 8 <= nb) {
 #pragma unroll
@@ -838,10 +862,10 @@ __global__ __launch_bounds__(512, 4) void k_mx4_gemm_mid4(const uint8_t *__restr
             __syncthreads();
 #pragma unroll
         for (int i = 0; i < CX; ++i)
-            lds.in.x[group][swizzled(row0 + 16 * i, q)] = xr[i];
+            lds.in.x[group][swizzled(row0 + GT / 8 * i, q)] = xr[i];
 #pragma unroll
         for (int i = 0; i < CW; ++i)
-            lds.in.w[group][swizzled(row0 + 16 * i, q)] = wr[i];
+            lds.in.w[group][swizzled(row0 + GT / 8 * i, q)] = wr[i];
         if (gt < BN)
             lds.in.ws[group][gt] = sr;
         else if (gt < BN + BM)
@@ -866,19 +890,27 @@ __global__ __launch_bounds__(512, 4) void k_mx4_gemm_mid4(const uint8_t *__restr
         kstep.template operator()<3>();
     }
     __syncthreads();
-    add_groups<TY, MT>(lds.red, acc, group, wn, r, h, Y, m0, n0, M, out);
+    add_groups<G, TY, MT>(lds.red, acc, group, wn, r, h, Y, m0, n0, M, out);
 }
 
 inline int64_t tiles_of(int64_t n, int64_t size) { return (n + size - 1) / size; }
 // Whole multiples of 8: see tile_of_block.
 inline uint32_t tile_grid(int64_t tiles) { return (uint32_t)((tiles + 7) / 8 * 8); }
 
-// Whether 64-token tiles of 64 rows beat 32-token ones: a block's time is about
-// 1 to 0.6, and a unit does its blocks one after another.
-inline bool mid_by_64(int64_t M, int64_t out)
+// The tiles of the kernels for mid sizes. 32 tokens x 32 rows where that makes no
+// more than a block a unit (16-bit, 64 x 4096x4096: 9.7 us, 64 x 64 tiles 12.4;
+// 64 x 4096x14336: 23, 34; 128 x 4096x4096, 512 such blocks: 17.0, and 12.8 by
+// 32 x 64). Else 64 tokens x 64 rows or 32: a block's time is about 1 to 0.6,
+// and a unit does its blocks one after another.
+template <typename F> void mid_shape(int64_t M, int64_t out, F run)
 {
     const int64_t n = tiles_of(out, 64), two = tiles_of(tiles_of(M, 64) * n, 256), one = tiles_of(tiles_of(M, 32) * n, 256);
-    return M > 32 && two * 10 <= one * 6;
+    if (tiles_of(M, 32) * tiles_of(out, 32) <= 256)
+        run.template operator()<1, 8>(tile_grid(tiles_of(M, 32) * tiles_of(out, 32)));
+    else if (M > 32 && two * 10 <= one * 6)
+        run.template operator()<2, 4>(tile_grid(tiles_of(M, 64) * n));
+    else
+        run.template operator()<1, 4>(tile_grid(tiles_of(M, 32) * n));
 }
 
 template <typename TX, typename TY>
@@ -904,12 +936,17 @@ hipError_t gemm(const TX *X, int64_t M, int nb, const uint8_t *codes, const uint
     if ((large <= 256 ? 80 : 100 * tiles_of(large, 512)) < 31 * small)
         k_mx4_gemm_tile<TX, TY><<<tile_grid(tiles_of(M, 128) * tiles_of(out, 256)), 256, 0, st>>>(X, M, nb, codes, scales,
                                                                                                 out, Y);
-    else if (mid_by_64(M, out))
-        k_mx4_gemm_mid<TX, TY, 2><<<tile_grid(tiles_of(M, 64) * tiles_of(out, 64)), 512, 0, st>>>(X, M, nb, codes, scales,
-                                                                                                out, Y);
     else
-        k_mx4_gemm_mid<TX, TY, 1><<<tile_grid(tiles_of(M, 32) * tiles_of(out, 64)), 512, 0, st>>>(X, M, nb, codes, scales,
-                                                                                                out, Y);
+        mid_shape(M, out, [&]<int MT, int G>(uint32_t blocks) {
+            // two blocks a unit against one with two buffers (4096 columns: 512
+            // blocks 30 us, 33; 256 blocks 19.6, 17.8)
+            if constexpr (MT == 2)
+                if (blocks > 256) {
+                    k_mx4_gemm_mid<TX, TY, MT, G, 1><<<blocks, 512, 0, st>>>(X, M, nb, codes, scales, out, Y);
+                    return;
+                }
+            k_mx4_gemm_mid<TX, TY, MT, G, 2><<<blocks, 512, 0, st>>>(X, M, nb, codes, scales, out, Y);
+        });
     return hipGetLastError();
 }
 
@@ -923,12 +960,10 @@ hipError_t gemm_a4(const uint8_t *xc, const uint8_t *xs, int64_t M, int nb, cons
     if (3 * tiles_of(tiles_of(M, 256) * tiles_of(out, 256), 256) < tiles_of(tiles_of(M, 64) * tiles_of(out, 64), 512))
         k_mx4_gemm_tile4<TY><<<tile_grid(tiles_of(M, 256) * tiles_of(out, 256)), 512, 0, st>>>(xc, xs, M, nb, codes,
                                                                                              scales, out, Y);
-    else if (mid_by_64(M, out))
-        k_mx4_gemm_mid4<TY, 2><<<tile_grid(tiles_of(M, 64) * tiles_of(out, 64)), 512, 0, st>>>(xc, xs, M, nb, codes,
-                                                                                             scales, out, Y);
     else
-        k_mx4_gemm_mid4<TY, 1><<<tile_grid(tiles_of(M, 32) * tiles_of(out, 64)), 512, 0, st>>>(xc, xs, M, nb, codes,
-                                                                                             scales, out, Y);
+        mid_shape(M, out, [&]<int MT, int G>(uint32_t blocks) {
+            k_mx4_gemm_mid4<TY, MT, G><<<blocks, 512, 0, st>>>(xc, xs, M, nb, codes, scales, out, Y);
+        });
     return hipGetLastError();
 }
 
