@@ -622,9 +622,9 @@ __device__ __forceinline__ uint32_t own_scales(const u32x2 &s, int h)
 
 // MXFP4 activations. Block: 256 x 256, 8 waves of 128 x 64. A stage is 256
 // columns, 128 bytes of codes of every row, in one of two LDS buffers; scales
-// come by four stages, 32 bytes of a row, into one buffer (a load of scales
-// costs a load unit the same whatever its width). What comes next is on its way
-// to registers meanwhile. (Four waves of 128 x 128 read a third less from LDS,
+// come by four stages, 32 bytes of a row, into one of two halves (a load of
+// scales costs a load unit the same whatever its width). What comes next is on
+// its way to registers meanwhile. (Four waves of 128 x 128 read a third less from LDS,
 // but alone on their SIMDs they wait for it.)
 // Lane (r, h) holds in k-step s of 4 block 2 s + h of its row.
 template <typename TY>
@@ -636,7 +636,7 @@ __global__ __launch_bounds__(512, 2) void k_mx4_gemm_tile4(const uint8_t *__rest
 {
     constexpr int MT = 4, NT = 2, B = 256, CH = 4;
     __shared__ __align__(16) u32x4 lx[2][B * 8], lw[2][B * 8];
-    __shared__ u32x2 ls[4][2 * B];                     // scales: activation rows, then weight rows
+    __shared__ u32x2 ls[8][2 * B];                     // scales of stage k at k & 7: activation rows, then weight rows
 
     int64_t m0, n0;
     if (!tile_of_block((M + B - 1) / B, (out + B - 1) / B, m0, n0))
@@ -683,10 +683,10 @@ __global__ __launch_bounds__(512, 2) void k_mx4_gemm_tile4(const uint8_t *__rest
         for (int i = 0; i < 4; ++i)
             sr[i] = load_scales8(sp, 8 * (k + i), nb);
     };
-    auto stash_s = [&] {
+    auto stash_s = [&](int k) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            ls[i][threadIdx.x] = sr[i];
+            ls[(k & 4) + i][threadIdx.x] = sr[i];
     };
     auto stash = [&](int k) {
         if (8 * k + q >= nb)
@@ -707,64 +707,76 @@ __global__ __launch_bounds__(512, 2) void k_mx4_gemm_tile4(const uint8_t *__rest
         for (int b = 0; b < NT; ++b)
             acc[a][b] = f32x16{};
 
+    // k-step s + 1's operands are read while k-step s is multiplied, and the last
+    // k-step of a stage is multiplied behind the barrier, while the first
+    // operands of the next stage are on their way.
+    uint32_t sa[MT], sb[NT];
+    u32x4 x[2][MT], w[2][NT];
+    auto read_s = [&](int k) {
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+            sa[a] = own_scales(ls[k & 7][128 * wm + 32 * a + r], h);
+#pragma unroll
+        for (int b = 0; b < NT; ++b)
+            sb[b] = own_scales(ls[k & 7][B + 64 * wn + 32 * b + r], h);
+    };
+    auto read = [&](int k, int s) {
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+            x[s & 1][a] = lx[k & 1][swizzled(128 * wm + 32 * a + r, 2 * s + h)];
+#pragma unroll
+        for (int b = 0; b < NT; ++b)
+            w[s & 1][b] = lw[k & 1][swizzled(64 * wn + 32 * b + r, 2 * s + h)];
+        asm volatile("" ::: "memory");                 // in this order: two sets of operands, no more
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto multiply = [&]<int S>() {
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+#pragma unroll
+            for (int b = 0; b < NT; ++b)
+                acc[a][b] = mfma32<S>(x[S & 1][a], sa[a], w[S & 1][b], sb[b], acc[a][b]);
+        // here, not after all reads of the stage (the products have no place of
+        // their own among the memory accesses)
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+#pragma unroll
+            for (int b = 0; b < NT; ++b)
+                asm volatile("" : "+v"(acc[a][b])::"memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
     fetch(0);
     fetch_s(0);
     stash(0);
-    stash_s();
+    stash_s(0);
+    if (1 < stages)
+        fetch(1);
     __syncthreads();
+    read_s(0);
+    read(0, 0);
+#pragma unroll 1
     for (int k = 0; k < stages; ++k) {
-        if (k + 1 < stages)
-            fetch(k + 1);
-        if ((k & 3) == 0 && k + 4 < stages)
-            fetch_s(k + 4);
-        uint32_t sa[MT], sb[NT];
-#pragma unroll
-        for (int a = 0; a < MT; ++a)
-            sa[a] = own_scales(ls[k & 3][128 * wm + 32 * a + r], h);
-#pragma unroll
-        for (int b = 0; b < NT; ++b)
-            sb[b] = own_scales(ls[k & 3][B + 64 * wn + 32 * b + r], h);
-        // k-step s + 1's operands are read while k-step s is multiplied
-        u32x4 x[2][MT], w[2][NT];
-        auto read = [&](int s) {
-#pragma unroll
-            for (int a = 0; a < MT; ++a)
-                x[s & 1][a] = lx[k & 1][swizzled(128 * wm + 32 * a + r, 2 * s + h)];
-#pragma unroll
-            for (int b = 0; b < NT; ++b)
-                w[s & 1][b] = lw[k & 1][swizzled(64 * wn + 32 * b + r, 2 * s + h)];
-        };
-        auto kstep = [&]<int S>() {
-            if (S < 3)
-                read(S + 1);
-            asm volatile("" ::: "memory");             // in this order: two sets of operands, no more
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int a = 0; a < MT; ++a)
-#pragma unroll
-                for (int b = 0; b < NT; ++b)
-                    acc[a][b] = mfma32<S>(x[S & 1][a], sa[a], w[S & 1][b], sb[b], acc[a][b]);
-            // here, not after all reads of the stage (the products have no
-            // place of their own among the memory accesses)
-#pragma unroll
-            for (int a = 0; a < MT; ++a)
-#pragma unroll
-                for (int b = 0; b < NT; ++b)
-                    asm volatile("" : "+v"(acc[a][b])::"memory");
-            __builtin_amdgcn_sched_barrier(0);
-        };
-        read(0);
-        kstep.template operator()<0>();
-        kstep.template operator()<1>();
-        kstep.template operator()<2>();
-        kstep.template operator()<3>();
-        if (k + 1 < stages)
+        if ((k & 3) == 1 && (k | 3) + 1 < stages)
+            fetch_s((k | 3) + 1);
+        read(k, 1);
+        multiply.template operator()<0>();
+        read(k, 2);
+        multiply.template operator()<1>();
+        read(k, 3);
+        if (k + 1 < stages) {
             stash(k + 1);
-        __syncthreads();
-        if ((k & 3) == 3 && k + 1 < stages) {          // everyone has read the last of the scales
-            stash_s();
-            __syncthreads();
+            if ((k & 3) == 3)
+                stash_s(k + 1);
+            if (k + 2 < stages)
+                fetch(k + 2);
         }
+        multiply.template operator()<2>();
+        __syncthreads();
+        if (k + 1 < stages)
+            read(k + 1, 0);
+        multiply.template operator()<3>();
+        if (k + 1 < stages)
+            read_s(k + 1);
     }
     // every wave is past its last read of the operands
     store_tiles<TY, MT>(Y, acc, reinterpret_cast<float *>(lx) + 2048 * wave, m0 + 128 * wm, n0 + 64 * wn, M, out, lane);
