@@ -307,7 +307,10 @@ hipError_t launch_mx4_gemm_a4(const uint8_t *xcodes, const uint8_t *xscales, int
 // How the down product of awq_mx4_moe is launched (see k_mx4_moe_down): blocks
 // over the hidden columns, parts of the contraction. `groups`: of one expert's
 // 16 tokens at most, as many as there can be; more of them never make fewer
-// parts.
+// parts. Narrow for few tokens with few units (microseconds of a whole layer
+// narrow, wide: 1 token, 8 of 64 experts of 2048x1024, 16 units 24.5, 33; 4
+// tokens of it, 64 units 42, 45; 1 token, 2 of 8 of 4096x14336, 56 units 60, 63;
+// 2 tokens of it, 112 units 97, 85; 16 tokens of it 242, 180).
 struct Mx4DownPlan {
     bool wide;
     int waves, blocks, parts;
@@ -316,7 +319,7 @@ inline Mx4DownPlan mx4_down_plan(int64_t M, int64_t hidden, int64_t inter, int64
 {
     const int64_t tiles = hidden / 16, units = groups * ((inter + 511) / 512);
     Mx4DownPlan p;
-    p.wide = M > 4;
+    p.wide = M > 4 || units > 64;
     int64_t parts;
     if (!p.wide) {
         p.waves = 16;

@@ -8,6 +8,11 @@
 // infinity or NaN is the byte of a NaN block. The conversion instruction
 // multiplies by a power of two, which is exact, rounds once to nearest even
 // and saturates at 6.
+//
+// All are bound by HBM, one load of 16 bytes (fp32: 32) a thread four times in
+// flight. 28672x4096, 2 bytes a value there and 0.53 here: quantize 54 us (5.5
+// TB/s), with s 52, dequantize 52; fp32: 98, 97 and 96 us (5.5 TB/s); a copy of
+// 2 GiB runs at 4.9. 2048x4096 takes 6 us, of which a launch is 2-3.
 #include "mx4.h"
 
 namespace awq {
@@ -101,7 +106,8 @@ __global__ __launch_bounds__(kThreads) void k_mx4_quantize_s(const T *__restrict
     }
 }
 
-// Values a thread makes of one load of codes: 16 bytes of them.
+// The values that a thread makes of one load of codes, 16 bytes, so that lanes
+// store whole lines (fp32 by 32 bytes a lane: 121 us where this takes 96).
 template <typename T> struct Piece {
     typedef uint32_t word;
     static __device__ __forceinline__ typename Vec8<T>::type make(word w, float s)

@@ -4,7 +4,18 @@
 // e2m1 * 2^E exactly (fp16 for E in [-13, 13]; elsewhere the fp16 activations
 // go as two exact bf16 parts), so the only roundings are those of the fp32
 // sums. With MXFP4 activations the scaled matrix instruction takes codes and
-// scale bytes as they are.
+// scale bytes as they are. bf16 and fp16 tokens cost the same unless an fp16
+// product meets such scales: then its share of the work is done a second time,
+// at half the rate (a zero block's scale, 2^-127, is one of them).
+//
+// What the forms reach (bf16 unless said; weights from HBM):
+//   split   1 token    x 4096x4096     5.3 us (a launch alone is 2-3)
+//   gemv    4 tokens   x 28672x4096   16 us, 3.9 TB/s
+//   mid     64 tokens  x 4096x4096     9.7 us
+//   mid     256 tokens x 4096x4096    17.8 us, 480 TFLOP/s
+//   tile    2048 tokens x 28672x4096  412 us, 1170 TFLOP/s
+//   mid4    256 tokens x 4096x4096    10.6 us, 810 TFLOP/s
+//   tile4   2048 tokens x 28672x4096  164 us, 2930 TFLOP/s
 #include "mx4.h"
 
 namespace awq {
@@ -20,9 +31,12 @@ __device__ __forceinline__ void store_tile(TY *Y, int64_t m, int64_t n, int64_t 
             Y[(m + i) * out + n] = static_cast<TY>(v[i]);
 }
 
-// Up to 16 tokens, 16-bit activations. Block: 16 rows, the columns split over W
-// waves in items of 128 U, each wave's next item in flight while it multiplies
-// the current one. The waves' sums are added in wave order through LDS.
+// Up to 16 tokens, 16-bit activations, few rows. Block: 16 rows, the columns
+// split over W waves in items of 128 U, each wave's next item in flight while it
+// multiplies the current one. The waves' sums are added in wave order through
+// LDS. Bound by latency: 4096x4096 is two items a wave (1 token 5.3 us, 16
+// tokens 8.0); with many tokens by the loads of their rows (4096x14336: 1 token
+// 12.4 us, 16 tokens 21.6).
 template <typename TX, typename TY, int U, int W>
 __global__ __launch_bounds__(64 * W) void k_mx4_gemm_split(const TX *__restrict__ X, int M, int nb,
                                                            const uint8_t *__restrict__ codes,
@@ -50,7 +64,8 @@ template <typename TX, typename TY, int U, int W>
 hipError_t split(const TX *X, int M, int nb, const uint8_t *codes, const uint8_t *scales, int64_t out, TY *Y,
                  hipStream_t st)
 {
-    k_mx4_gemm_split<TX, TY, U, W><<<dim3((uint32_t)((out + 15) / 16)), 64 * W, 0, st>>>(X, M, nb, codes, scales, out, Y);
+    k_mx4_gemm_split<TX, TY, U, W><<<dim3((uint32_t)((out + 15) / 16)), 64 * W, 0, st>>>(X, M, nb, codes, scales, out,
+                                                                                        Y);
     return hipGetLastError();
 }
 
@@ -59,7 +74,8 @@ hipError_t split(const TX *X, int M, int nb, const uint8_t *codes, const uint8_t
 // units for a whole block each. Block: 8 / S row tiles of 16, all columns, S
 // waves a tile; the activations go through LDS in chunks of kc blocks that all
 // waves share. Every wave streams its own weights (see StreamItem), the next
-// item in flight also across the chunks' barriers.
+// item in flight also across the chunks' barriers. Bound by HBM: 28672x4096 (62
+// MB) 16 us, 3.9 TB/s, where a plain read of as much reaches 6.
 template <typename TX, typename TY, int S>
 __global__ __launch_bounds__(512, 4) void k_mx4_gemv(const TX *__restrict__ X, int M, int nb, int kc,
                                                      const uint8_t *__restrict__ codes,
@@ -246,7 +262,9 @@ __device__ __forceinline__ int swizzled(int row, int q) { return row * 8 + (q ^ 
 // use. What comes next is on its way to registers meanwhile; activations have
 // two buffers, so a step costs one barrier, and a fourth one more. Weights are
 // converted by the wave that multiplies them (no other one has its rows), once
-// for 128 tokens.
+// for 128 tokens. 2048 tokens x 28672x4096: 412 us, 1170 TFLOP/s (8192 tokens:
+// 1225), the matrix units busy for 56 % of it; a dense bf16 library product of
+// the shape takes 398 us.
 // Lane (r, h) = (lane % 32, lane / 32) of a 32-row tile holds in k-step s of 4
 // columns 32 h + 8 s ... of the step: chunk 4 h + s of an activation row, word
 // s of block h of a weight row.
@@ -466,11 +484,13 @@ __device__ __forceinline__ void add_groups(float (&red)[G / 2][32 * MT][256 / G]
 // of which each group takes 64; the groups' sums meet in LDS. Such shapes leave
 // one block or two on a unit, so a round's loads go out two rounds ahead. BUF
 // LDS buffers: two need one barrier a round, one leaves room for a second block.
+// A round's loads and its LDS accesses, about 500 cycles each for 32 x 64, are
+// what bounds it, and waits where they do not overlap (203 tokens x 4097x4064
+// 19.7 us, 343 TFLOP/s; 64 tokens x 4096x14336 23 us).
 template <typename TX, typename TY, int MT, int G, int BUF>
-__global__ __launch_bounds__(512, BUF == 2 && MT * G == 8 ? 2 : 4) void k_mx4_gemm_mid(const TX *__restrict__ X, int64_t M, int nb,
-                                                         const uint8_t *__restrict__ codes,
-                                                         const uint8_t *__restrict__ scales, int64_t out,
-                                                         TY *__restrict__ Y)
+__global__ __launch_bounds__(512, BUF == 2 && MT * G == 8 ? 2 : 4) void k_mx4_gemm_mid(
+    const TX *__restrict__ X, int64_t M, int nb, const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales,
+    int64_t out, TY *__restrict__ Y)
 {
     typedef typename Vec8<TX>::type vec;
     constexpr int BM = 32 * MT, BN = 256 / G, GT = 512 / G;     // GT: threads of a group
@@ -522,7 +542,8 @@ __global__ __launch_bounds__(512, BUF == 2 && MT * G == 8 ? 2 : 4) void k_mx4_ge
     auto fetch = [&](Round &to, int j) {
         if (j >= rounds)
             return;
-        const int b0 = 2 * G * j, xb = b0 + 2 * group + (q >> 2), xover = (xb - (nb - 1)) * 64;     // its block of the row
+        const int b0 = 2 * G * j, xb = b0 + 2 * group + (q >> 2);      // xb: its block of the row
+        const int xover = (xb - (nb - 1)) * 64;
         const int wover = (b0 + wq - (nb - 1)) * 16;
         const uint8_t *const px = xbase + (int64_t)b0 * 64 + group * 128, *const pw = wbase + (int64_t)b0 * 16;
 #pragma unroll
@@ -624,8 +645,10 @@ __device__ __forceinline__ uint32_t own_scales(const u32x2 &s, int h)
 // columns, 128 bytes of codes of every row, in one of two LDS buffers; scales
 // come by four stages, 32 bytes of a row, into one of two halves (a load of
 // scales costs a load unit the same whatever its width). What comes next is on
-// its way to registers meanwhile. (Four waves of 128 x 128 read a third less from LDS,
-// but alone on their SIMDs they wait for it.)
+// its way to registers meanwhile. (Four waves of 128 x 128 read a third less from
+// LDS, but alone on their SIMDs they wait for it.) 2048 tokens x 28672x4096: 164
+// us, 2930 TFLOP/s. A stage is 2048 cycles of the matrix units and 2500 of LDS,
+// which overlap in part (3700).
 // Lane (r, h) holds in k-step s of 4 block 2 s + h of its row.
 template <typename TY>
 __global__ __launch_bounds__(512, 2) void k_mx4_gemm_tile4(const uint8_t *__restrict__ xcodes,
@@ -785,6 +808,9 @@ __global__ __launch_bounds__(512, 2) void k_mx4_gemm_tile4(const uint8_t *__rest
 // MXFP4 activations, too few 256 x 256 tiles for the chip, or few tokens. Block:
 // 32 MT tokens x 256 / G rows, 8 waves: G groups of 32 rows a wave. A round is
 // 256 G columns, of which each group takes 256; the groups' sums meet in LDS.
+// 256 tokens x 4096x4096 10.6 us (four rounds: latency), 256 tokens x 4096x14336
+// 28.7 us, 1050 TFLOP/s: bound by a round's loads and LDS accesses one after the
+// other. (A second buffer and loads two rounds ahead: 11.1 and 27.1 us.)
 template <typename TY, int MT, int G>
 __global__ __launch_bounds__(512, 4) void k_mx4_gemm_mid4(const uint8_t *__restrict__ xcodes,
                                                           const uint8_t *__restrict__ xscales, int64_t M, int nb,
@@ -916,7 +942,8 @@ inline uint32_t tile_grid(int64_t tiles) { return (uint32_t)((tiles + 7) / 8 * 8
 // and a unit does its blocks one after another.
 template <typename F> void mid_shape(int64_t M, int64_t out, F run)
 {
-    const int64_t n = tiles_of(out, 64), two = tiles_of(tiles_of(M, 64) * n, 256), one = tiles_of(tiles_of(M, 32) * n, 256);
+    const int64_t n = tiles_of(out, 64);
+    const int64_t two = tiles_of(tiles_of(M, 64) * n, 256), one = tiles_of(tiles_of(M, 32) * n, 256);
     if (tiles_of(M, 32) * tiles_of(out, 32) <= 256)
         run.template operator()<1, 8>(tile_grid(tiles_of(M, 32) * tiles_of(out, 32)));
     else if (M > 32 && two * 10 <= one * 6)
@@ -932,7 +959,9 @@ hipError_t gemm(const TX *X, int64_t M, int nb, const uint8_t *codes, const uint
     if (M <= 16) {
         // Enough row tiles for more than a block's worth a unit: few waves a
         // tile (28672 rows of 4096, 4 tokens: S = 1, 2, 4, 8 take 16.4, 15.7,
-        // 17.9, 21.1 us; 12288 rows, 2 tokens: 14.4, 10.3, 9.7, 10.9).
+        // 17.9, 21.1 us; 12288 rows, 2 tokens: 14.4, 10.3, 9.7, 10.9). Above 16
+        // tokens `mid`: with 16 x 28672x4096 it takes 22 us, gemv 19; with 16 x
+        // 4096x14336 19, split 21.6, but 8 tokens 17.2 both, 1 token 16.8, 12.4.
         const int64_t tiles = tiles_of(out, 16);
         if (tiles >= 1280)
             return gemv<TX, TY, 2>(X, (int)M, nb, codes, scales, out, Y, st);
@@ -944,10 +973,10 @@ hipError_t gemm(const TX *X, int64_t M, int nb, const uint8_t *codes, const uint
     // the small tiles and each further 512; large ones 80 us for up to 256 (one
     // a unit), 100 for each 512 (1024 x 4096 rows: 60 us small, 80 large; 2048 x
     // 4096: 120, 79)
-    const int64_t large = tiles_of(M, 128) * tiles_of(out, 256), small = tiles_of(tiles_of(M, 64) * tiles_of(out, 64), 512);
+    const int64_t large = tiles_of(M, 128) * tiles_of(out, 256);
+    const int64_t small = tiles_of(tiles_of(M, 64) * tiles_of(out, 64), 512);
     if ((large <= 256 ? 80 : 100 * tiles_of(large, 512)) < 31 * small)
-        k_mx4_gemm_tile<TX, TY><<<tile_grid(tiles_of(M, 128) * tiles_of(out, 256)), 256, 0, st>>>(X, M, nb, codes, scales,
-                                                                                                out, Y);
+        k_mx4_gemm_tile<TX, TY><<<tile_grid(large), 256, 0, st>>>(X, M, nb, codes, scales, out, Y);
     else
         mid_shape(M, out, [&]<int MT, int G>(uint32_t blocks) {
             // two blocks a unit against one with two buffers (4096 columns: 512
@@ -966,9 +995,9 @@ template <typename TY>
 hipError_t gemm_a4(const uint8_t *xc, const uint8_t *xs, int64_t M, int nb, const uint8_t *codes, const uint8_t *scales,
                    int64_t out, TY *Y, hipStream_t st)
 {
-    // 256 x 256 tiles or 64 x 64 ones: 4096 columns take 40 us for each 256 of the
-    // large, 13 for each 512 of the small (1024 x 4096 rows: 26 us small, 38
-    // large; 2048 x 4096: 52, 40)
+    // 256 x 256 tiles or 64 x 64 ones: 4096 columns take 36 us for each 256 of the
+    // large, 13 for each 512 of the small (1024 x 4096 rows: 28 us small, 35
+    // large; 2048 x 4096: 52, 36)
     if (3 * tiles_of(tiles_of(M, 256) * tiles_of(out, 256), 256) < tiles_of(tiles_of(M, 64) * tiles_of(out, 64), 512))
         k_mx4_gemm_tile4<TY><<<tile_grid(tiles_of(M, 256) * tiles_of(out, 256)), 512, 0, st>>>(xc, xs, M, nb, codes,
                                                                                              scales, out, Y);
