@@ -310,7 +310,7 @@ hipError_t launch_mx4_gemm_a4(const uint8_t *xcodes, const uint8_t *xscales, int
 // parts. Narrow for few tokens with few units (microseconds of a whole layer
 // narrow, wide: 1 token, 8 of 64 experts of 2048x1024, 16 units 24.5, 33; 4
 // tokens of it, 64 units 42, 45; 1 token, 2 of 8 of 4096x14336, 56 units 60, 63;
-// 2 tokens of it, 112 units 97, 85; 16 tokens of it 242, 180).
+// 2 tokens of it, 112 units 98, 97; 4 tokens 143, 130; 16 tokens 242, 180).
 struct Mx4DownPlan {
     bool wide;
     int waves, blocks, parts;

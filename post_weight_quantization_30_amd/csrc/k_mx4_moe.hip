@@ -12,7 +12,7 @@
 // of routed experts is found by every block from the routing's ids (at most 64 x
 // 16 of them).
 //
-//   1 token, 8 of 64 experts of 2048x1024     24.5 us (28 MB): logits 2.6, up
+//   1 token, 8 of 64 experts of 2048x1024     24.5 us (27 MB): logits 2.6, up
 //                                             12.3 with the routing, down 9.6
 //   8 tokens, 2 of 8 of 4096x14336            160 us (748 MB, 4.7 TB/s): up 100
 //                                             (5.0 TB/s), down 57 (4.4)
