@@ -13,9 +13,9 @@
 //   gemv    4 tokens   x 28672x4096   16 us, 3.9 TB/s
 //   mid     64 tokens  x 4096x4096     9.7 us
 //   mid     256 tokens x 4096x4096    17.8 us, 480 TFLOP/s
-//   tile    2048 tokens x 28672x4096  412 us, 1170 TFLOP/s
+//   tile    2048 tokens x 28672x4096  405 us, 1190 TFLOP/s
 //   mid4    256 tokens x 4096x4096    10.6 us, 810 TFLOP/s
-//   tile4   2048 tokens x 28672x4096  164 us, 2930 TFLOP/s
+//   tile4   2048 tokens x 28672x4096  162 us, 2970 TFLOP/s
 #include "mx4.h"
 
 namespace awq {
@@ -173,16 +173,17 @@ __device__ __forceinline__ f32x16 mfma32(const u32x4 &a, uint32_t sa, const u32x
 }
 
 // Tile of this block: the blocks of one XCD (every eighth) walk a contiguous
-// range of tiles, 16 token tiles by one row tile at a time, so that what they
-// read together stays in that XCD's L2.
+// range of tiles, 4 token tiles by one row tile at a time, so that what they
+// read together stays in that XCD's L2 (the 64 tiles that an XCD has in work read
+// 13 MB then; by 16 token tiles 18: 2048 x 28672x4096 16-bit 405 us, 420).
 __device__ __forceinline__ bool tile_of_block(int64_t tm, int64_t tn, int64_t &m, int64_t &n)
 {
     const int64_t tiles = tm * tn, chunk = (tiles + 7) / 8;
     const int64_t t = (blockIdx.x & 7) * chunk + (blockIdx.x >> 3);
     if ((blockIdx.x >> 3) >= chunk || t >= tiles)
         return false;
-    const int64_t band = t / (16 * tn), first = band * 16, in_band = t - band * 16 * tn;
-    const int64_t h = tm - first < 16 ? tm - first : 16;
+    const int64_t band = t / (4 * tn), first = band * 4, in_band = t - band * 4 * tn;
+    const int64_t h = tm - first < 4 ? tm - first : 4;
     m = first + in_band % h;
     n = in_band / h;
     return true;
@@ -262,8 +263,8 @@ __device__ __forceinline__ int swizzled(int row, int q) { return row * 8 + (q ^ 
 // use. What comes next is on its way to registers meanwhile; activations have
 // two buffers, so a step costs one barrier, and a fourth one more. Weights are
 // converted by the wave that multiplies them (no other one has its rows), once
-// for 128 tokens. 2048 tokens x 28672x4096: 412 us, 1170 TFLOP/s (8192 tokens:
-// 1225), the matrix units busy for 56 % of it; a dense bf16 library product of
+// for 128 tokens. 2048 tokens x 28672x4096: 405 us, 1190 TFLOP/s (8192 tokens:
+// 1230), the matrix units busy for 56 % of it; a dense bf16 library product of
 // the shape takes 398 us.
 // Lane (r, h) = (lane % 32, lane / 32) of a 32-row tile holds in k-step s of 4
 // columns 32 h + 8 s ... of the step: chunk 4 h + s of an activation row, word
@@ -646,8 +647,8 @@ __device__ __forceinline__ uint32_t own_scales(const u32x2 &s, int h)
 // come by four stages, 32 bytes of a row, into one of two halves (a load of
 // scales costs a load unit the same whatever its width). What comes next is on
 // its way to registers meanwhile. (Four waves of 128 x 128 read a third less from
-// LDS, but alone on their SIMDs they wait for it.) 2048 tokens x 28672x4096: 164
-// us, 2930 TFLOP/s. A stage is 2048 cycles of the matrix units and 2500 of LDS,
+// LDS, but alone on their SIMDs they wait for it: 181 us.) 2048 tokens x 28672x4096: 162
+// us, 2970 TFLOP/s. A stage is 2048 cycles of the matrix units and 2500 of LDS,
 // which overlap in part (3700).
 // Lane (r, h) holds in k-step s of 4 block 2 s + h of its row.
 template <typename TY>
