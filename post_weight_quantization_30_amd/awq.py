@@ -380,23 +380,25 @@ MX4_BLOCK = 32                     # columns that share an MXFP4 scale
 MX4_MOE_MAX_TOKENS, MX4_MOE_MAX_TOPK, MX4_MOE_MAX_EXPERTS = 64, 16, 256
 
 
-def _launch(name, device, *args):
-    """Calls the library on `device` and the stream that is current there."""
-    fn, index = getattr(lib(), name), device.index
-    if index == torch.cuda.current_device():
+def _launch(name, index, *args):
+    """Calls the library on GPU `index` and the stream that is current there."""
+    fn = getattr(_lib or lib(), name)
+    if index == torch._C._cuda_getDevice():
         status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(index):
             status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
-    _check(name, status)
+    if status != OK:
+        raise AwqError(name, status)
 
 
-def _ptr(t, name, device=None, dtype=None):
-    """Address of a contiguous GPU tensor (on `device`, of `dtype`)."""
-    if not t.is_cuda:
+def _ptr(t, name, index=None, dtype=None):
+    """Address of a contiguous GPU tensor (on GPU `index`, of `dtype`)."""
+    at = t.get_device()
+    if at < 0:
         raise TypeError(f"{name} must be a GPU tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if index is not None and at != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got cuda:{at}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
@@ -407,7 +409,8 @@ def _ptr(t, name, device=None, dtype=None):
 def _mx4_cols(codes, scales, what=""):
     """Columns of an MXFP4 matrix (codes uint8 (..., in / 2), scales uint8 (..., in / 32))."""
     c, s = codes.shape, scales.shape
-    if len(c) < 2 or len(s) != len(c) or c[-1] * 2 != s[-1] * MX4_BLOCK or c[0] != s[0] or c[1:-1] != s[1:-1]:
+    if (len(c) < 2 or len(s) != len(c) or c[-1] * 2 != s[-1] * MX4_BLOCK or c[0] != s[0]
+            or len(c) > 2 and c[1:-1] != s[1:-1]):
         raise ValueError(f"{what}codes must be (..., in / 2) and {what}scales (..., in / {MX4_BLOCK})")
     return c[-1] * 2
 
@@ -418,24 +421,24 @@ def mx4_quantize(W, s=None, codes=None, scales=None):
     shape = W.shape
     if len(shape) < 2 or shape[-1] % MX4_BLOCK != 0:
         raise ValueError(f"W must be (..., in) with in a multiple of {MX4_BLOCK}")
-    n_in, dev, rows = shape[-1], W.device, shape[0] if len(shape) == 2 else math.prod(shape[:-1])
-    cshape, sshape = (*shape[:-1], n_in // 2), (*shape[:-1], n_in // MX4_BLOCK)
+    n_in, dev, at, outer = shape[-1], W.device, W.get_device(), shape[:-1]
+    rows, cshape, sshape = math.prod(outer), (*outer, n_in // 2), (*outer, n_in // MX4_BLOCK)
     codes = torch.empty(*cshape, dtype=torch.uint8, device=dev) if codes is None else _need(codes, "codes", cshape)
     scales = torch.empty(*sshape, dtype=torch.uint8, device=dev) if scales is None else _need(scales, "scales", sshape)
     if s is not None:
-        s = _ptr(_need(s, "s", (n_in,)), "s", dev, torch.float32)
-    _launch("awq_mx4_quantize", dev, _ptr(W, "W"), _dtype_code(W), rows, n_in, s,
-            _ptr(codes, "codes", dev, torch.uint8), _ptr(scales, "scales", dev, torch.uint8))
+        s = _ptr(_need(s, "s", (n_in,)), "s", at, torch.float32)
+    _launch("awq_mx4_quantize", at, _ptr(W, "W"), _dtype_code(W), rows, n_in, s,
+            _ptr(codes, "codes", at, torch.uint8), _ptr(scales, "scales", at, torch.uint8))
     return codes, scales
 
 
 def mx4_dequantize(codes, scales, dtype=torch.bfloat16, out=None):
     """The values (..., in) that MXFP4 codes and scales stand for, as `dtype`."""
-    n_in, dev = _mx4_cols(codes, scales), codes.device
-    shape = (*codes.shape[:-1], n_in)
-    out = torch.empty(*shape, dtype=dtype, device=dev) if out is None else _need(out, "out", shape)
-    _launch("awq_mx4_dequantize", dev, _ptr(codes, "codes", None, torch.uint8),
-            _ptr(scales, "scales", dev, torch.uint8), math.prod(shape[:-1]), n_in, _ptr(out, "out", dev),
+    n_in, at, outer = _mx4_cols(codes, scales), codes.get_device(), codes.shape[:-1]
+    shape = (*outer, n_in)
+    out = torch.empty(*shape, dtype=dtype, device=codes.device) if out is None else _need(out, "out", shape)
+    _launch("awq_mx4_dequantize", at, _ptr(codes, "codes", None, torch.uint8),
+            _ptr(scales, "scales", at, torch.uint8), math.prod(outer), n_in, _ptr(out, "out", at),
             _dtype_code(out))
     return out
 
@@ -446,11 +449,11 @@ def mx4_gemm(X, codes, scales, y=None, y_f32=False):
     M, n_in = X.shape
     if codes.dim() != 2 or _mx4_cols(codes, scales) != n_in:
         raise ValueError("codes must be (out, in / 2) for X (M, in)")
-    out, dev = codes.shape[0], X.device
+    out, at = codes.shape[0], X.get_device()
     ydt = torch.float32 if y_f32 else X.dtype
-    y = torch.empty(M, out, dtype=ydt, device=dev) if y is None else _need(y, "y", (M, out))
-    _launch("awq_mx4_gemm", dev, _ptr(X, "X"), _dtype_code(X), M, n_in, _ptr(codes, "codes", dev, torch.uint8),
-            _ptr(scales, "scales", dev, torch.uint8), out, _ptr(y, "y", dev, ydt), _DTYPE[ydt])
+    y = torch.empty(M, out, dtype=ydt, device=X.device) if y is None else _need(y, "y", (M, out))
+    _launch("awq_mx4_gemm", at, _ptr(X, "X"), _dtype_code(X), M, n_in, _ptr(codes, "codes", at, torch.uint8),
+            _ptr(scales, "scales", at, torch.uint8), out, _ptr(y, "y", at, ydt), _DTYPE[ydt])
     return y
 
 
@@ -460,11 +463,11 @@ def mx4_gemm_a4(x_codes, x_scales, codes, scales, dtype=torch.bfloat16, y=None):
     n_in = _mx4_cols(x_codes, x_scales, "x_")
     if x_codes.dim() != 2 or codes.dim() != 2 or _mx4_cols(codes, scales) != n_in:
         raise ValueError("x_codes must be (M, in / 2) and codes (out, in / 2)")
-    M, out, dev = x_codes.shape[0], codes.shape[0], x_codes.device
-    y = torch.empty(M, out, dtype=dtype, device=dev) if y is None else _need(y, "y", (M, out))
-    _launch("awq_mx4_gemm_a4", dev, _ptr(x_codes, "x_codes", None, torch.uint8),
-            _ptr(x_scales, "x_scales", dev, torch.uint8), M, n_in, _ptr(codes, "codes", dev, torch.uint8),
-            _ptr(scales, "scales", dev, torch.uint8), out, _ptr(y, "y", dev, dtype), _dtype_code(y))
+    M, out, at = x_codes.shape[0], codes.shape[0], x_codes.get_device()
+    y = torch.empty(M, out, dtype=dtype, device=x_codes.device) if y is None else _need(y, "y", (M, out))
+    _launch("awq_mx4_gemm_a4", at, _ptr(x_codes, "x_codes", None, torch.uint8),
+            _ptr(x_scales, "x_scales", at, torch.uint8), M, n_in, _ptr(codes, "codes", at, torch.uint8),
+            _ptr(scales, "scales", at, torch.uint8), out, _ptr(y, "y", at, dtype), _dtype_code(y))
     return y
 
 
@@ -486,13 +489,13 @@ def mx4_moe(X, router, gate_up, gate_up_scales, down, down_scales, top_k, renorm
     _need(router, "router", (experts, hidden))
     _need(gate_up, "gate_up", (experts, 2 * inter, hidden // 2))
     _need(down, "down", (experts, hidden, inter // 2))
-    dev, u8 = X.device, torch.uint8
+    dev, at, u8 = X.device, X.get_device(), torch.uint8
     y = torch.empty_like(X) if y is None else _need(y, "y", (M, hidden))
     ws = _workspace(mx4_moe_workspace_size(M, hidden, inter, top_k), dev, workspace)
-    _launch("awq_mx4_moe", dev, _ptr(X, "X"), _dtype_code(X), M, hidden, inter, experts, top_k, int(bool(renorm)),
-            _ptr(router, "router", dev, X.dtype), _ptr(gate_up, "gate_up", dev, u8),
-            _ptr(gate_up_scales, "gate_up_scales", dev, u8), _ptr(down, "down", dev, u8),
-            _ptr(down_scales, "down_scales", dev, u8), _ptr(y, "y", dev, X.dtype), _ptr(ws, "workspace", dev),
+    _launch("awq_mx4_moe", at, _ptr(X, "X"), _dtype_code(X), M, hidden, inter, experts, top_k, int(bool(renorm)),
+            _ptr(router, "router", at, X.dtype), _ptr(gate_up, "gate_up", at, u8),
+            _ptr(gate_up_scales, "gate_up_scales", at, u8), _ptr(down, "down", at, u8),
+            _ptr(down_scales, "down_scales", at, u8), _ptr(y, "y", at, X.dtype), _ptr(ws, "workspace", at),
             ws.numel() * ws.element_size())
     return y
 
