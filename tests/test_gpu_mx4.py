@@ -158,7 +158,11 @@ def operands(awq, M, out, n, dt, seed):
 GEMM = [(1, 1, 32), (1, 300, 512), (2, 17, 96), (5, 64, 4096), (16, 48, 608), (15, 1000, 14336), (17, 130, 1024),
         (33, 65, 32), (64, 64, 2080), (70, 20, 256), (200, 515, 1120), (256, 4096, 512), (257, 511, 544),
         (1000, 700, 1056), (515, 3000, 128), (2100, 4100, 160), (2047, 4097, 544), (4100, 2050, 32),
-        (4, 20490, 160), (16, 10250, 608), (1, 10241, 96)]
+        (4, 20490, 160), (16, 10250, 608), (1, 10241, 96),
+        # tiles of mid sizes over many rounds: 32 x 32, 32 x 64, 64 x 64 once and twice a unit
+        (40, 2000, 4128), (17, 4090, 3232), (97, 5000, 2080), (250, 4090, 1184), (505, 4090, 672),
+        # large tiles of one stage to many, their last one ragged
+        (2050, 4097, 256), (2050, 4097, 1312), (2100, 4100, 2624)]
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
@@ -300,7 +304,12 @@ MOE = [(1, 8, 2, 256, 512, "bf16", True), (1, 1, 1, 32, 32, "f16", False), (2, 6
        (7, 130, 16, 544, 64, "f16", False), (40, 3, 2, 4096, 224, "bf16", True), (64, 70, 1, 288, 544, "f16", False),
        # few hidden columns (waves without any), many parts, one expert for all
        (5, 6, 3, 32, 1056, "bf16", True), (20, 9, 4, 32, 608, "f16", True), (64, 1, 1, 96, 2592, "bf16", True),
-       (6, 4, 4, 160, 4128, "f16", False), (16, 40, 2, 1088, 96, "bf16", True)]
+       (6, 4, 4, 160, 4128, "f16", False), (16, 40, 2, 1088, 96, "bf16", True),
+       # as many experts and choices as there may be, with and without a launch for the routing
+       (8, 256, 16, 96, 64, "f16", False), (9, 256, 16, 96, 64, "bf16", True), (1, 200, 9, 2048, 96, "bf16", False),
+       # one, two and four waves a tile; few tokens with many units
+       (8, 16, 8, 544, 1056, "f16", True), (9, 16, 8, 544, 1600, "bf16", True), (12, 16, 8, 544, 2080, "f16", False),
+       (2, 3, 2, 64, 16416, "bf16", True), (4, 5, 2, 288, 8224, "f16", True)]
 
 
 def moe_inputs(M, E, hidden, inter, dt, seed):
@@ -439,11 +448,12 @@ def test_moe_refuses_a_short_workspace(awq):
 
 # ---- streams and graphs ---------------------------------------------------------
 
-def test_graph_replays(awq):
+@pytest.mark.parametrize("M", [1, 9])
+def test_graph_replays(awq, M):
     """Quantise, multiply and a mixture-of-experts layer captured once on a side
     stream, replayed on new inputs, eager work between the replays."""
-    say("graph")
-    M, hidden, inter, E, k = 9, 256, 128, 6, 2
+    say("graph", M)
+    hidden, inter, E, k = 256, 128, 6, 2
     X, X32, R, R32, gu, dn = moe_inputs(M, E, hidden, inter, "bf16", 60)
     _, _, gcd, gsd = mx4(awq, gu)
     _, _, dcd, dsd = mx4(awq, dn)
@@ -464,7 +474,7 @@ def test_graph_replays(awq):
     with torch.cuda.graph(g):
         got = layer(static)
     for i in range(4):
-        x = torch.roll(X, i, 0) * (1 + i)
+        x = torch.roll(X, i, 1) * (1 + i)
         static.copy_(x)
         g.replay()
         want = layer(x)
