@@ -332,7 +332,9 @@ inline Mx4DownPlan mx4_down_plan(int64_t M, int64_t hidden, int64_t inter, int64
             if ((tiles + w - 1) / w * w < (tiles + p.waves - 1) / p.waves * p.waves)
                 p.waves = w;
         p.blocks = (int)((tiles + p.waves - 1) / p.waves);
-        parts = units / 4 < 256 / p.blocks ? units / 4 : 256 / p.blocks;   // four units a wave or more
+        // a unit a wave or more (29 tokens, 4 of 4 experts of 416x576: 28 us a layer,
+        // by four units 38; 8 tokens, 2 of 8 of 1024x1024: 24.5, 31.5)
+        parts = units < 256 / p.blocks ? units : 256 / p.blocks;
     }
     p.parts = (int)(parts < 1 ? 1 : parts > 64 ? 64 : parts);
     return p;
