@@ -31,8 +31,8 @@ constexpr int kMaxTok = AWQ_MX4_MOE_MAX_TOKENS, kMaxK = AWQ_MX4_MOE_MAX_TOPK, kM
 // Logits: a block per expert and TOK tokens, its four waves and their lanes
 // along the columns. (A router row is read in whole kilobytes: 16 rows of 64
 // bytes, as a matrix tile would read them, keep a load unit busy twice as long.)
-// Bound by latency: 2.6 us for 1 token, 64 experts of 2048 columns, 4.7 for 8
-// tokens, 8 experts of 4096; one block for 16 tokens took 11.
+// Bound by latency: 2.6 us for 1 token, 64 experts of 2048 columns; one block
+// for all experts of 16 tokens took 11.
 template <typename TX, int TOK>
 __global__ __launch_bounds__(256) void k_mx4_moe_logits(const TX *__restrict__ X, int M, int hidden,
                                                         const TX *__restrict__ router, int E,
@@ -644,9 +644,11 @@ hipError_t moe(const void *X, int M, int hidden, int inter, int E, int top_k, in
     bf16 *const h = (bf16 *)(ws + lay.h_off);
     const TX *const x = (const TX *)X, *const rw = (const TX *)router;
     const int pairs = M * top_k, most = (pairs < E ? pairs : E) + (M > 16 ? pairs / 16 : 0);   // groups at most
-    if (M == 1)
+    // Tokens a block: as many as still leave about a block a unit (a layer of 5
+    // tokens, 8 experts of 1024x1024: one a block 22.5 us, four 23.2, eight 23.9).
+    if (E * M <= 256)
         logits<TX, 1>(x, M, hidden, rw, E, lg, st);
-    else if (M <= 4)
+    else if (M <= 4 || E * ((M + 7) / 8) <= 256)
         logits<TX, 4>(x, M, hidden, rw, E, lg, st);
     else
         logits<TX, 8>(x, M, hidden, rw, E, lg, st);
