@@ -6,7 +6,7 @@
 // sums. With MXFP4 activations the scaled matrix instruction takes codes and
 // scale bytes as they are. bf16 and fp16 tokens cost the same unless an fp16
 // product meets such scales: then its share of the work is done a second time,
-// at half the rate (a zero block's scale, 2^-127, is one of them).
+// at half the rate (blocks of zeros do not count).
 //
 // What the forms reach (bf16 unless said; weights from HBM):
 //   split   1 token    x 4096x4096     5.3 us (a launch alone is 2-3)
@@ -316,7 +316,7 @@ __global__ __launch_bounds__(256, 2) void k_mx4_gemm_tile(const TX *__restrict__
     f32x16 acc[MT][NT];
     u32x4 xr[CX], wr[CW];
     u32x2 wsr, ws[NT];
-    bool bad = false;
+    F16Range range;
 
     // Past a row's end (in its last step or stretch) the last chunk there is is
     // loaded instead; zeros take its place among the activations, 127 (2^0)
@@ -381,7 +381,7 @@ __global__ __launch_bounds__(256, 2) void k_mx4_gemm_tile(const TX *__restrict__
                 w[b] = lw[swizzled(64 * wave + 32 * b + r, 2 * part + h)];
                 byte[b] = (part & 2 ? ws[b][1] : ws[b][0]) >> (16 * (part & 1) + 8 * h) & 0xFFu;
                 if constexpr (std::is_same<TX, f16>::value && !WIDE)
-                    bad = bad || !mx4_fits_f16(byte[b]);
+                    range.see(w[b], byte[b]);
             }
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
@@ -433,7 +433,7 @@ __global__ __launch_bounds__(256, 2) void k_mx4_gemm_tile(const TX *__restrict__
     // fp16 activations under scales that fp16 cannot hold: all of it once more
     // in the wide form (weights in bf16, activations as two bf16 parts)
     if constexpr (std::is_same<TX, f16>::value)
-        if (__syncthreads_or(bad))
+        if (__syncthreads_or(range.exceeded()))
             contract.template operator()<true>();
     // every wave is past its last read of the operands
     store_tiles<TY, MT>(Y, acc, reinterpret_cast<float *>(lx) + 2048 * wave, m0, n0 + 64 * wave, M, out, lane);
@@ -538,7 +538,7 @@ __global__ __launch_bounds__(512, BUF == 2 && MT * G == 8 ? 2 : 4) void k_mx4_ge
         u32x4 x[CX], w;
         u32x2 ws;
     } even, odd;
-    bool bad = false;
+    F16Range range;
 
     auto fetch = [&](Round &to, int j) {
         if (j >= rounds)
@@ -584,7 +584,7 @@ __global__ __launch_bounds__(512, BUF == 2 && MT * G == 8 ? 2 : 4) void k_mx4_ge
             const u32x2 ws = in.ws[group >> 2][32 * wn + r];
             const uint32_t byte = (group & 2 ? ws[1] : ws[0]) >> (16 * (group & 1) + 8 * h) & 0xFFu;
             if constexpr (std::is_same<TX, f16>::value && !WIDE)
-                bad = bad || !mx4_fits_f16(byte);
+                range.see(w, byte);
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
                 vec wv;
@@ -629,7 +629,7 @@ __global__ __launch_bounds__(512, BUF == 2 && MT * G == 8 ? 2 : 4) void k_mx4_ge
     };
     contract.template operator()<false>();
     if constexpr (std::is_same<TX, f16>::value)
-        if (__syncthreads_or(bad))                     // scales that fp16 cannot hold
+        if (__syncthreads_or(range.exceeded()))                     // scales that fp16 cannot hold
             contract.template operator()<true>();
 
     add_groups<G, TY, MT>(lds.red, acc, group, wn, r, h, Y, m0, n0, M, out);

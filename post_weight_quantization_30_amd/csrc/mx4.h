@@ -43,7 +43,7 @@ __device__ __forceinline__ bf16x8 mx4_to_bf16(uint32_t w, float s)
     return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// The eight codes of one word as fp16: exact where mx4_fits_f16(byte).
+// The eight codes of one word as fp16: exact where F16Range holds the block to fit.
 __device__ __forceinline__ f16x8 mx4_to_f16(uint32_t w, float s)
 {
     const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 0);
@@ -53,21 +53,18 @@ __device__ __forceinline__ f16x8 mx4_to_f16(uint32_t w, float s)
     return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// fp16 holds 0.5 * 2^E .. 6 * 2^E as normal numbers for E in [-13, 13].
-__device__ __forceinline__ bool mx4_fits_f16(uint32_t byte) { return byte - 114u <= 26u; }
-
-// Whether all scale bytes seen fit fp16, four at a time: the largest byte - 114
-// as unsigned halves.
+// fp16 holds 0.5 * 2^E .. 6 * 2^E as normal numbers for E in [-13, 13]:
+// whether the blocks seen are such, by the largest byte - 114 of those that hold
+// anything but zeros. (A block of zeros has byte 0, a block of NaN 255, and the
+// conversion makes NaN of that whatever the codes.)
 struct F16Range {
-    typedef uint16_t half2 __attribute__((ext_vector_type(2)));
-    half2 worst = {0, 0};
-    __device__ __forceinline__ void see(uint32_t bytes)
+    uint32_t worst = 0;
+    __device__ __forceinline__ void see(const u32x4 &block, uint32_t byte)
     {
-        const half2 from = {114, 114};
-        worst = __builtin_elementwise_max(worst, __builtin_bit_cast(half2, bytes & 0x00FF00FFu) - from);
-        worst = __builtin_elementwise_max(worst, __builtin_bit_cast(half2, bytes >> 8 & 0x00FF00FFu) - from);
+        const uint32_t over = ((block[0] | block[1] | block[2] | block[3]) & 0x77777777u) ? byte - 114u : 0;
+        worst = worst > over ? worst : over;
     }
-    __device__ __forceinline__ bool exceeded() const { return worst[0] > 26 || worst[1] > 26; }
+    __device__ __forceinline__ bool exceeded() const { return worst > 26; }
 };
 
 // fp16 values as the exact sum of two bf16 parts (11 significand bits = 8 + 3;
@@ -160,12 +157,12 @@ __device__ __forceinline__ void mx4_load(Mx4Item<TX, U> &it, const Mx4Rows<TX> &
 // fp16 cannot hold: weights in bf16, activations as two bf16 parts. The plain
 // form notes the scales it meets in `range`.
 template <bool WIDE, typename TX, int U>
-__device__ __forceinline__ void mx4_compute(Mx4Item<TX, U> &it, f32x4 &acc, int b0, int nb, F16Range &range)
+__device__ __forceinline__ void mx4_compute(Mx4Item<TX, U> &it, f32x4 &acc, int b0, int nb, int c, F16Range &range)
 {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         if constexpr (std::is_same<TX, f16>::value && !WIDE)
-            range.see(it.ws[u]);
+            range.see(it.w[u], it.ws[u] >> (8 * c) & 0xFFu);
         transpose4(it.w[u]);
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
@@ -205,13 +202,13 @@ __device__ __forceinline__ void mx4_wave(const Mx4Rows<TX> &rows, f32x4 &acc, in
     while (true) {
         if (i + step < nb)
             mx4_load(b, rows, i + step, nb, c);
-        mx4_compute<false>(a, acc, i, nb, range);
+        mx4_compute<false>(a, acc, i, nb, c, range);
         i += step;
         if (i >= nb)
             break;
         if (i + step < nb)
             mx4_load(a, rows, i + step, nb, c);
-        mx4_compute<false>(b, acc, i, nb, range);
+        mx4_compute<false>(b, acc, i, nb, c, range);
         i += step;
         if (i >= nb)
             break;
@@ -222,7 +219,7 @@ __device__ __forceinline__ void mx4_wave(const Mx4Rows<TX> &rows, f32x4 &acc, in
 #pragma unroll 1
             for (i = first; i < nb; i += step) {
                 mx4_load(a, rows, i, nb, c);
-                mx4_compute<true>(a, acc, i, nb, range);
+                mx4_compute<true>(a, acc, i, nb, c, range);
             }
         }
     }
@@ -312,9 +309,9 @@ __device__ __forceinline__ void stream_compute(StreamItem<NT> &it, const TX *con
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             wu[nt] = it.w[nt][u];
-            transpose4(wu[nt]);
             if constexpr (std::is_same<TX, f16>::value && !WIDE)
-                range.see(it.s[nt][u]);
+                range.see(wu[nt], it.s[nt][u] >> (8 * c) & 0xFFu);
+            transpose4(wu[nt]);
         }
         if (ROLL && next_b0 >= 0)
             stream_load_w(it.w, u, next, next_b0, nb, c);

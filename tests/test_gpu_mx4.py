@@ -232,6 +232,24 @@ def test_gemm_a4_any_scale(awq, M, out):
     check(awq.mx4_gemm_a4(*d, dtype=torch.float32), Xq @ Wd.T, np.abs(Xq) @ np.abs(Wd).T, n, "f32", "a4 any scale")
 
 
+@pytest.mark.parametrize("M,out,n", [(3, 130, 672), (40, 130, 672), (300, 1030, 672), (1030, 4100, 672), (2, 10250, 1056),
+                                     (2, 20490, 1056)])
+def test_gemm_blocks_of_zeros(awq, M, out, n):
+    """Pruned and padded weights: zero blocks and rows, whose scale fp16 cannot hold."""
+    say("zeros", M, out, n)
+    X, W = operands(awq, M, out, n, "f16", 12)
+    W[:, -32:] = 0
+    W[::3, 64:96] = 0
+    W[7] = 0
+    Xd, X32 = store(X, "f16")
+    c, s, cd, sd = mx4(awq, W)
+    assert (s[:, -1] == 0).all()
+    Wd, X64 = mx.dequantize(c, s), X32.astype(np.float64)
+    Y = awq.mx4_gemm(Xd, cd, sd, y_f32=True)
+    check(Y, X64 @ Wd.T, np.abs(X64) @ np.abs(Wd).T, n, "f32", "zeros")
+    assert bool((Y[:, 7] == 0).all())
+
+
 @pytest.mark.parametrize("M,out", [(1, 70), (40, 70), (300, 70), (2100, 4100), (3, 10250), (2, 20490)])
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
 @pytest.mark.parametrize("n", [96, 1024])
