@@ -363,10 +363,15 @@ int awq_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows
  *   awq_mx4_gemm_a4: the same with X MXFP4 too (as awq_mx4_quantize writes it);
  *                    Y of y_dtype, any.
  * Operands enter the matrix cores without rounding and are summed in fp32 in a
- * fixed order (bitwise reproducible): each output is within
- * (in + 16) * 2^-24 * sum_k |X[m][k] W[n][k]| of the exact value, plus the
- * rounding to a 16-bit Y. A row of X or W that holds a NaN makes its own
+ * fixed order (bitwise reproducible): with S = sum_k |X[m][k] W[n][k]| below 2^127
+ * each output is within (in + 16) * (2^-24 * S + 2^-149) of the exact value (the
+ * second term is fp32's smallest step: products and sums may be subnormal), plus
+ * the rounding to a 16-bit Y. A row of X or W that holds a NaN makes its own
  * outputs NaN and no others.
+ * awq_mx4_gemm takes values below 2^128: scale byte 253 stands under magnitudes up
+ * to 3 and byte 254 under magnitudes up to 1.5 (awq_mx4_quantize writes neither
+ * byte). A larger value, which no 16-bit or fp32 number holds, makes the outputs
+ * of its row of W infinite or NaN, and no others. awq_mx4_gemm_a4 takes them all.
  * AWQ_ERR_UNSUPPORTED: x_dtype AWQ_F32, X or codes (xcodes) not 16-byte aligned,
  * M above 2 097 120, out above 2^28, `in` above 2^23, or M * out of 2^38 or more. */
 int awq_mx4_gemm(const void *X, int x_dtype, int64_t M, int64_t in, const uint8_t *codes,
@@ -393,7 +398,8 @@ int awq_mx4_gemm_a4(const uint8_t *xcodes, const uint8_t *xscales, int64_t M, in
  *           (0 for sizes that the call refuses). Calls that overlap in time need
  *           a workspace each.
  * hidden and inter must be multiples of 32, 1 <= top_k <= experts.
- * An expert's NaN or infinite values reach only the tokens routed to it.
+ * An expert's NaN values, and those of 2^128 or more (see above), reach only the
+ * tokens routed to it.
  * AWQ_ERR_UNSUPPORTED: dtype AWQ_F32, M > AWQ_MX4_MOE_MAX_TOKENS, top_k >
  * AWQ_MX4_MOE_MAX_TOPK, experts > AWQ_MX4_MOE_MAX_EXPERTS, hidden or inter above
  * 2^20, X, router, codes or ws not 16-byte aligned. */

@@ -32,8 +32,9 @@ constexpr int kMxBlock = 32;
 // exponent field only, 0 as 2^-127 and 255 as NaN.
 __device__ __forceinline__ float mx4_scale(uint32_t byte) { return __builtin_bit_cast(float, byte << 23); }
 
-// The eight codes of one word as bf16 (exact for every scale: three
-// significand bits at most, and bf16 reaches 2^-133).
+// The eight codes of one word as bf16: exact below 2^128 (two significand bits,
+// and bf16 reaches down to 2^-133; the matrix instructions take its subnormals).
+// 4 and 6 under byte 253 and 2 to 6 under byte 254 become infinities.
 __device__ __forceinline__ bf16x8 mx4_to_bf16(uint32_t w, float s)
 {
     const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0);
@@ -68,7 +69,8 @@ struct F16Range {
 };
 
 // fp16 values as the exact sum of two bf16 parts (11 significand bits = 8 + 3;
-// an infinity stays in the first part).
+// an infinity stays in the first part). A weight of 2^128 or more is an infinity
+// here: with a second part of zero it gives NaN.
 __device__ __forceinline__ void split_f16(const f16x8 &x, bf16x8 &hi, bf16x8 &lo)
 {
 #pragma unroll
