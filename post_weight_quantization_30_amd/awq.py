@@ -125,14 +125,28 @@ def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
-def _dev(t, name, dtype=None):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+def _index(t, name):
+    """The GPU that a tensor is on (-1: the host)."""
+    if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a GPU tensor")
+    return t.get_device()
+
+
+def _dev(t, name, dtype=None, index=None):
+    """Address of a contiguous GPU tensor (of `dtype`, on GPU `index`)."""
+    try:
+        at = t.get_device()
+    except AttributeError:                 # not a tensor
+        at = -1
+    if at < 0:
+        raise TypeError(f"{name} must be a GPU tensor")
+    if index is not None and at != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got cuda:{at}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _need(t, name, shape):
@@ -392,20 +406,6 @@ def _launch(name, index, *args):
         raise AwqError(name, status)
 
 
-def _ptr(t, name, index=None, dtype=None):
-    """Address of a contiguous GPU tensor (on GPU `index`, of `dtype`)."""
-    at = t.get_device()
-    if at < 0:
-        raise TypeError(f"{name} must be a GPU tensor")
-    if index is not None and at != index:
-        raise ValueError(f"{name} must be on cuda:{index}, got cuda:{at}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    return t.data_ptr()
-
-
 def _mx4_cols(codes, scales, what=""):
     """Columns of an MXFP4 matrix (codes uint8 (..., in / 2), scales uint8 (..., in / 32))."""
     c, s = codes.shape, scales.shape
@@ -421,24 +421,24 @@ def mx4_quantize(W, s=None, codes=None, scales=None):
     shape = W.shape
     if len(shape) < 2 or shape[-1] % MX4_BLOCK != 0:
         raise ValueError(f"W must be (..., in) with in a multiple of {MX4_BLOCK}")
-    n_in, dev, at, outer = shape[-1], W.device, W.get_device(), shape[:-1]
+    n_in, at, outer, dev = shape[-1], _index(W, "W"), shape[:-1], W.device
     rows, cshape, sshape = math.prod(outer), (*outer, n_in // 2), (*outer, n_in // MX4_BLOCK)
     codes = torch.empty(*cshape, dtype=torch.uint8, device=dev) if codes is None else _need(codes, "codes", cshape)
     scales = torch.empty(*sshape, dtype=torch.uint8, device=dev) if scales is None else _need(scales, "scales", sshape)
     if s is not None:
-        s = _ptr(_need(s, "s", (n_in,)), "s", at, torch.float32)
-    _launch("awq_mx4_quantize", at, _ptr(W, "W"), _dtype_code(W), rows, n_in, s,
-            _ptr(codes, "codes", at, torch.uint8), _ptr(scales, "scales", at, torch.uint8))
+        s = _dev(_need(s, "s", (n_in,)), "s", torch.float32, at)
+    _launch("awq_mx4_quantize", at, _dev(W, "W"), _dtype_code(W), rows, n_in, s,
+            _dev(codes, "codes", torch.uint8, at), _dev(scales, "scales", torch.uint8, at))
     return codes, scales
 
 
 def mx4_dequantize(codes, scales, dtype=torch.bfloat16, out=None):
     """The values (..., in) that MXFP4 codes and scales stand for, as `dtype`."""
-    n_in, at, outer = _mx4_cols(codes, scales), codes.get_device(), codes.shape[:-1]
+    n_in, at, outer = _mx4_cols(codes, scales), _index(codes, "codes"), codes.shape[:-1]
     shape = (*outer, n_in)
     out = torch.empty(*shape, dtype=dtype, device=codes.device) if out is None else _need(out, "out", shape)
-    _launch("awq_mx4_dequantize", at, _ptr(codes, "codes", None, torch.uint8),
-            _ptr(scales, "scales", at, torch.uint8), math.prod(outer), n_in, _ptr(out, "out", at),
+    _launch("awq_mx4_dequantize", at, _dev(codes, "codes", torch.uint8),
+            _dev(scales, "scales", torch.uint8, at), math.prod(outer), n_in, _dev(out, "out", None, at),
             _dtype_code(out))
     return out
 
@@ -447,13 +447,13 @@ def mx4_gemm(X, codes, scales, y=None, y_f32=False):
     """Y (M, out) = X W^T for MXFP4 weights W (out, in) and 16-bit X (M, in).
     Y is fp32 when y_f32, else X's dtype."""
     M, n_in = X.shape
-    if codes.dim() != 2 or _mx4_cols(codes, scales) != n_in:
+    if len(codes.shape) != 2 or _mx4_cols(codes, scales) != n_in:
         raise ValueError("codes must be (out, in / 2) for X (M, in)")
-    out, at = codes.shape[0], X.get_device()
+    out, at = codes.shape[0], _index(X, "X")
     ydt = torch.float32 if y_f32 else X.dtype
     y = torch.empty(M, out, dtype=ydt, device=X.device) if y is None else _need(y, "y", (M, out))
-    _launch("awq_mx4_gemm", at, _ptr(X, "X"), _dtype_code(X), M, n_in, _ptr(codes, "codes", at, torch.uint8),
-            _ptr(scales, "scales", at, torch.uint8), out, _ptr(y, "y", at, ydt), _DTYPE[ydt])
+    _launch("awq_mx4_gemm", at, _dev(X, "X"), _dtype_code(X), M, n_in, _dev(codes, "codes", torch.uint8, at),
+            _dev(scales, "scales", torch.uint8, at), out, _dev(y, "y", ydt, at), _DTYPE[ydt])
     return y
 
 
@@ -461,13 +461,13 @@ def mx4_gemm_a4(x_codes, x_scales, codes, scales, dtype=torch.bfloat16, y=None):
     """Y (M, out) = X W^T as `dtype`, X (M, in) and W (out, in) both MXFP4 (X as
     mx4_quantize writes it)."""
     n_in = _mx4_cols(x_codes, x_scales, "x_")
-    if x_codes.dim() != 2 or codes.dim() != 2 or _mx4_cols(codes, scales) != n_in:
+    if len(x_codes.shape) != 2 or len(codes.shape) != 2 or _mx4_cols(codes, scales) != n_in:
         raise ValueError("x_codes must be (M, in / 2) and codes (out, in / 2)")
-    M, out, at = x_codes.shape[0], codes.shape[0], x_codes.get_device()
+    M, out, at = x_codes.shape[0], codes.shape[0], _index(x_codes, "x_codes")
     y = torch.empty(M, out, dtype=dtype, device=x_codes.device) if y is None else _need(y, "y", (M, out))
-    _launch("awq_mx4_gemm_a4", at, _ptr(x_codes, "x_codes", None, torch.uint8),
-            _ptr(x_scales, "x_scales", at, torch.uint8), M, n_in, _ptr(codes, "codes", at, torch.uint8),
-            _ptr(scales, "scales", at, torch.uint8), out, _ptr(y, "y", at, dtype), _dtype_code(y))
+    _launch("awq_mx4_gemm_a4", at, _dev(x_codes, "x_codes", torch.uint8),
+            _dev(x_scales, "x_scales", torch.uint8, at), M, n_in, _dev(codes, "codes", torch.uint8, at),
+            _dev(scales, "scales", torch.uint8, at), out, _dev(y, "y", dtype, at), _dtype_code(y))
     return y
 
 
@@ -483,19 +483,19 @@ def mx4_moe(X, router, gate_up, gate_up_scales, down, down_scales, top_k, renorm
     (experts, hidden, inter / 2); scales as mx4_quantize writes them."""
     M, hidden = X.shape
     experts = router.shape[0]
-    if gate_up.dim() != 3 or down.dim() != 3 or _mx4_cols(gate_up, gate_up_scales, "gate_up_") != hidden:
+    if len(gate_up.shape) != 3 or len(down.shape) != 3 or _mx4_cols(gate_up, gate_up_scales, "gate_up_") != hidden:
         raise ValueError("gate_up must be (experts, 2 inter, hidden / 2)")
     inter = _mx4_cols(down, down_scales, "down_")
     _need(router, "router", (experts, hidden))
     _need(gate_up, "gate_up", (experts, 2 * inter, hidden // 2))
     _need(down, "down", (experts, hidden, inter // 2))
-    dev, at, u8 = X.device, X.get_device(), torch.uint8
+    at, u8 = _index(X, "X"), torch.uint8
     y = torch.empty_like(X) if y is None else _need(y, "y", (M, hidden))
-    ws = _workspace(mx4_moe_workspace_size(M, hidden, inter, top_k), dev, workspace)
-    _launch("awq_mx4_moe", at, _ptr(X, "X"), _dtype_code(X), M, hidden, inter, experts, top_k, int(bool(renorm)),
-            _ptr(router, "router", at, X.dtype), _ptr(gate_up, "gate_up", at, u8),
-            _ptr(gate_up_scales, "gate_up_scales", at, u8), _ptr(down, "down", at, u8),
-            _ptr(down_scales, "down_scales", at, u8), _ptr(y, "y", at, X.dtype), _ptr(ws, "workspace", at),
+    ws = _workspace(mx4_moe_workspace_size(M, hidden, inter, top_k), X.device, workspace)
+    _launch("awq_mx4_moe", at, _dev(X, "X"), _dtype_code(X), M, hidden, inter, experts, top_k, int(bool(renorm)),
+            _dev(router, "router", X.dtype, at), _dev(gate_up, "gate_up", u8, at),
+            _dev(gate_up_scales, "gate_up_scales", u8, at), _dev(down, "down", u8, at),
+            _dev(down_scales, "down_scales", u8, at), _dev(y, "y", X.dtype, at), _dev(ws, "workspace", None, at),
             ws.numel() * ws.element_size())
     return y
 
