@@ -343,9 +343,13 @@ size_t awq_gptq_workspace_size(int64_t out, int64_t in);
  * -127), byte = e + 127; a code has v's sign and |v| * 2^-e rounded to the
  * nearest magnitude, ties to the even code, 6 above 6. Bit-exact. A block with
  * an infinity or a NaN gets byte 255 and codes 0.
- *   W: device (rows, in) of `dtype`, 16-byte aligned; e.g. a layer's weights
- *      (s: device fp32[in], 16-byte aligned, as s_best of awq_search, or NULL),
+ *   W: device (rows, in) of `dtype`, 16-byte aligned; e.g. a layer's weights,
  *      several layers' or experts' stacked, or activations.
+ *   s: device fp32[in], 16-byte aligned, or NULL; e.g. a row of awq_s_table. Choose
+ *      it by this format's error: s_best of awq_search makes the error of integer
+ *      groups least and may do worse here than no s (the headline recipe at
+ *      512x1024: output error 0.00850 with s_best, 0.00825 without, 0.00819 at
+ *      the best row of the same table).
  * awq_mx4_dequantize: out (rows, in) of `dtype` = the values, rounded to nearest
  * even where `dtype` does not hold them (bf16 and fp32 hold all below 2^128).
  * Outputs must not overlap inputs, here and in the calls below.

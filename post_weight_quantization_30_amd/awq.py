@@ -417,7 +417,8 @@ def _mx4_cols(codes, scales, what=""):
 
 def mx4_quantize(W, s=None, codes=None, scales=None):
     """W (..., in) to MXFP4 along its last dimension: (codes uint8 (..., in / 2),
-    scales uint8 (..., in / 32)); with `s` (fp32 [in]) of W diag(s)."""
+    scales uint8 (..., in / 32)); with `s` (fp32 [in]) of W diag(s), an s chosen by
+    this format's error (the search's is chosen by that of integer groups)."""
     shape = W.shape
     if len(shape) < 2 or shape[-1] % MX4_BLOCK != 0:
         raise ValueError(f"W must be (..., in) with in a multiple of {MX4_BLOCK}")
