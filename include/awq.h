@@ -370,7 +370,9 @@ int awq_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows
  * fixed order (bitwise reproducible): with S = sum_k |X[m][k] W[n][k]| below 2^127
  * each output is within (in + 16) * (2^-24 * S + 2^-149) of the exact value (the
  * second term is fp32's smallest step: products and sums may be subnormal), plus
- * the rounding to a 16-bit Y. A row of X or W that holds a NaN makes its own
+ * the rounding to a 16-bit Y. In S an operand that is subnormal in its 16-bit type
+ * (X below 2^-14 in fp16, X or W below 2^-126 in bf16) counts as the smallest normal
+ * number: the matrix cores align its products as if it were that large. A row of X or W that holds a NaN makes its own
  * outputs NaN and no others.
  * awq_mx4_gemm takes values below 2^128: scale byte 253 stands under magnitudes up
  * to 3 and byte 254 under magnitudes up to 1.5 (awq_mx4_quantize writes neither
@@ -390,8 +392,8 @@ int awq_mx4_gemm_a4(const uint8_t *xcodes, const uint8_t *xscales, int64_t M, in
  *   lowest index; a NaN ranks lowest); p = softmax(l) over all experts at those,
  *   divided by their sum if renorm is not 0;
  *   h_e = silu(Wgate_e x) * (Wup_e x);  y = sum_e p_e Wdown_e h_e.
- * Everything is fp32 up to Y but p_e h_e, which keeps 16 significant bits (and
- * fp32's range).
+ * Everything is fp32 up to Y (the products with the experts as above) but p_e h_e,
+ * which keeps 16 significant bits (and fp32's range).
  *   X:      device (M, hidden) of `dtype` (AWQ_F16 or AWQ_BF16), M <= AWQ_MX4_MOE_MAX_TOKENS.
  *   router: device (experts, hidden) of `dtype`.
  *   gu_codes, gu_scales: device, the MXFP4 matrix (experts * 2 * inter, hidden): of each

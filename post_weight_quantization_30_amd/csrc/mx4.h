@@ -54,10 +54,13 @@ __device__ __forceinline__ f16x8 mx4_to_f16(uint32_t w, float s)
     return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// fp16 holds 0.5 * 2^E .. 6 * 2^E as normal numbers for E in [-13, 13]:
-// whether the blocks seen are such, by the largest byte - 114 of those that hold
-// anything but zeros. (A block of zeros has byte 0, a block of NaN 255, and the
-// conversion makes NaN of that whatever the codes.)
+// fp16 holds 0.5 * 2^E .. 6 * 2^E as normal numbers for E in [-13, 13]: whether
+// the blocks seen are such, by the largest byte - 114 of those that hold anything
+// but zeros. (A block of zeros has byte 0, a block of NaN 255, and the conversion
+// makes NaN of that whatever the codes.) Subnormal fp16 weights, exact down to
+// E = -23, would not do: the matrix instruction aligns their products as those of
+// 2^-14, and 3 tokens x 20490 rows of 96 columns under E = -23 to -14 came out
+// wrong by 270 * 2^-24 of sum |x w|.
 struct F16Range {
     uint32_t worst = 0;
     __device__ __forceinline__ void see(const u32x4 &block, uint32_t byte)
@@ -189,8 +192,8 @@ __device__ __forceinline__ void mx4_compute(Mx4Item<TX, U> &it, f32x4 &acc, int 
 
 // The items that begin at blocks first, first + step, ... of the rows, each in
 // flight while the one before it is multiplied. fp16 activations: where a scale
-// turns out not to fit, all of it once more in the wide form (real weights
-// never need it, so the hot loop carries no branch and no registers for it).
+// turns out not to fit, all of it once more in the wide form, so that the hot
+// loop carries no branch for it.
 template <int U, typename TX>
 __device__ __forceinline__ void mx4_wave(const Mx4Rows<TX> &rows, f32x4 &acc, int first, int step, int nb, int c)
 {

@@ -3,7 +3,9 @@ weights and activations, blocks that fp16 cannot hold in the experts' weights.
 
 Bounds as in test_gpu_mx4.py. Where products or sums fall below fp32's normal
 numbers a rounding is off by at most a step of its subnormals, 2^-149, instead of
-2^-24 of the sum: (n + 16) (u S + 2^-149).
+2^-24 of the sum: (n + 16) (u S + 2^-149). The matrix instructions align products by
+their operands' exponents and a subnormal operand has that of the smallest normal
+number: there S counts the operand as that number.
 Each test prints the case it runs (flushed) before touching the GPU.
 """
 import numpy as np
@@ -105,10 +107,11 @@ def test_gemm_bytes_253_and_254(awq, M, out, n, dt):
 
 
 @pytest.mark.parametrize("M,out,n", SHAPES)
-@pytest.mark.parametrize("lo,hi", [(114, 140), (113, 140), (114, 141)])
+@pytest.mark.parametrize("lo,hi", [(114, 140), (113, 140), (114, 141), (104, 140), (103, 140), (104, 141)])
 def test_gemm_f16_at_its_borders(awq, M, out, n, lo, hi):
-    """fp16 weights are used for bytes 114 to 140: just these, their ends in every row,
-    and one step past either end; activations are subnormal but in the last columns."""
+    """fp16 holds weights under bytes 104 to 140, from 114 on as normal numbers, and is
+    used for these: the ends of both ranges in every row, and one step past either
+    end; activations are subnormal but in the last columns."""
     say("fp16 borders", M, out, n, lo, hi)
     r = np.random.default_rng(24)
     c = r.integers(0, 256, (out, n // 2)).astype(np.uint8)
@@ -118,6 +121,49 @@ def test_gemm_f16_at_its_borders(awq, M, out, n, lo, hi):
     X[:, -32:] *= 2.0 ** 10
     Xd, X32 = store(X, "f16")
     assert (np.abs(X32[:, :-32]) < 2.0 ** -13).all() and (X32[:, :-32] != 0).any()
+    want, S = product(X32, mx.dequantize(c, s))
+    worst = far(awq.mx4_gemm(Xd, *dev(c, s), y_f32=True), want, S, n)
+    say("max err/bound", float(worst.max()))
+    assert (worst <= 1).all()
+
+
+@pytest.mark.parametrize("dt,tiny,bits,lo,hi", [("f16", 2.0 ** -14, 10, 114, 140), ("bf16", 2.0 ** -126, 7, 190, 250)])
+@pytest.mark.parametrize("M,out,n", SHAPES + [(2, 130, 64)])
+def test_gemm_subnormal_activations(awq, M, out, n, dt, tiny, bits, lo, hi):
+    """Nothing but subnormal activations, from the largest to the smallest. The first
+    token has the smallest alone: in the first 32 columns, and in one behind them,
+    where the weights of each row are larger by another power of two."""
+    say("subnormal activations", M, out, n, dt)
+    r = np.random.default_rng(27)
+    c = r.integers(0, 256, (out, n // 2)).astype(np.uint8)
+    s = r.integers(lo, hi + 1, (out, n // 32)).astype(np.uint8)
+    s[:, 0], s[:, 1] = lo + np.arange(out) % (hi - lo + 1), hi
+    c[:, :16], c[:, 16] = 0x33, 0x11                       # 1.5 in the first block, 0.5 in the column
+    k = np.maximum(r.integers(1, 2 ** bits, (M, n)) >> r.integers(0, bits, (M, 1)), 1) * r.choice([-1, 1], (M, n))
+    k[0] = 0
+    k[0, :32] = k[0, 32] = 1
+    Xd, X32 = store(k * (tiny * 2.0 ** -bits), dt)
+    assert (X32 == k * (tiny * 2.0 ** -bits)).all()
+    Wd = mx.dequantize(c, s)
+    want, S = product(X32, Wd)
+    raised = np.where(X32 == 0, 0.0, np.maximum(np.abs(X32), tiny)) @ np.abs(Wd).T
+    Y = awq.mx4_gemm(Xd, *dev(c, s), y_f32=True)
+    say("max err/bound", float(far(Y, want, raised, n).max()), "with S itself", float(far(Y, want, S, n).max()))
+    assert (far(Y, want, raised, n) <= 1).all()
+
+
+@pytest.mark.parametrize("M,out,n", SHAPES)
+def test_gemm_f16_subnormal_weights(awq, M, out, n):
+    """Rows whose weights would all be subnormal in fp16, down to its smallest, under
+    large activations (the matrix instruction would lose bits of them); others of
+    larger ones."""
+    say("fp16 subnormal", M, out, n)
+    r = np.random.default_rng(26)
+    c = r.integers(0, 256, (out, n // 2)).astype(np.uint8)
+    lo, hi = np.array([[104, 104], [104, 113], [112, 116]])[np.arange(out) % 3].T
+    s = r.integers(lo[:, None], hi[:, None] + 1, (out, n // 32)).astype(np.uint8)
+    X = r.standard_normal((M, n)) * np.exp2(r.integers(0, 12, (1, n)))
+    Xd, X32 = store(X, "f16")
     want, S = product(X32, mx.dequantize(c, s))
     worst = far(awq.mx4_gemm(Xd, *dev(c, s), y_f32=True), want, S, n)
     say("max err/bound", float(worst.max()))
@@ -199,6 +245,19 @@ def test_moe_blocks_that_fp16_cannot_hold(awq, M, E, k, hidden, inter, dt):
     if dt == "f16":                                        # keep the results in its range
         ds[:, 1::3, -1] = 125
     check_moe(awq, X, X32, R, R32, (gc, gs, dc, ds), k, True, dt)
+
+
+@pytest.mark.parametrize("M,E,k,hidden,inter", WIDE)
+def test_moe_f16_subnormal_weights(awq, M, E, k, hidden, inter):
+    """Gate and up weights that would be subnormal in fp16, under large activations."""
+    say("moe subnormal", M, E, k, hidden, inter)
+    r = np.random.default_rng(35)
+    gc, gs, dc, ds = experts(r, E, hidden, inter)
+    gs -= 13                                               # 106 to 108
+    gs[:, ::5, 0] = 104
+    X, X32 = store(r.standard_normal((M, hidden)) * 2.0 ** 13, "f16")
+    R, R32 = store(r.standard_normal((E, hidden)) * 1.5 * 2.0 ** -13 / hidden ** 0.5, "f16")
+    check_moe(awq, X, X32, R, R32, (gc, gs, dc, ds), k, True, "f16")
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
