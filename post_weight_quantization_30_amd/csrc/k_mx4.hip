@@ -10,9 +10,13 @@
 // and saturates at 6.
 //
 // All are bound by HBM, one load of 16 bytes (fp32: 32) a thread four times in
-// flight. 28672x4096, 2 bytes a value there and 0.53 here: quantize 54 us (5.5
-// TB/s), with s 52, dequantize 52; fp32: 98, 97 and 96 us (5.5 TB/s); a copy of
-// 2 GiB runs at 4.9. 2048x4096 takes 6 us, of which a launch is 2-3.
+// flight. 28672x4096, 2 bytes a value there and 0.53 here: quantize 53 us (5.6
+// TB/s), with s 52, dequantize 51; fp32: 99, 99 and 97 us (5.4 TB/s); a copy of
+// 2 GiB runs at 4.7 (both directions), a plain read at 6.1. 2048x4096 takes 6 to
+// 7 us, of which a launch is 2-3. With s a block's 256 threads take one stretch of
+// 2048 columns and those past the row idle: just above a multiple of 2048 and far
+// below it s costs time (28672 rows of 2080 fp16 39 us, without s 29; of 256 8.2,
+// 6.7; of 32 7.2, 3.3). Medians of graph replays over 600 MB of inputs in turn.
 #include "mx4.h"
 
 namespace awq {
@@ -107,7 +111,7 @@ __global__ __launch_bounds__(kThreads) void k_mx4_quantize_s(const T *__restrict
 }
 
 // The values that a thread makes of one load of codes, 16 bytes, so that lanes
-// store whole lines (fp32 by 32 bytes a lane: 121 us where this takes 96).
+// store whole lines (fp32 by 32 bytes a lane: 121 us where this takes 97).
 template <typename T> struct Piece {
     typedef uint32_t word;
     static __device__ __forceinline__ typename Vec8<T>::type make(word w, float s)

@@ -4,17 +4,27 @@
 // e2m1 * 2^E exactly (fp16 for E in [-13, 13]; elsewhere the fp16 activations
 // go as two exact bf16 parts), so the only roundings are those of the fp32
 // sums. With MXFP4 activations the scaled matrix instruction takes codes and
-// scale bytes as they are. bf16 and fp16 tokens cost the same unless an fp16
-// product meets such scales: then its share of the work is done a second time,
-// at half the rate (blocks of zeros do not count).
+// scale bytes as they are. bf16 and fp16 tokens cost about the same (fp16 7 % more
+// in `tile`) unless an fp16 product meets such scales: then its share of the work
+// is done a second time, at half the rate (blocks of zeros do not count). One
+// block of weights below 2^-11, and not 0, in one row of 64 takes 4 tokens x
+// 28672x4096 from 20 to 49 us, 64 x 4096x4096 from 10.8 to 21.5, 203 x 4097x4064
+// from 22 to 51, 2048 x 28672x4096 from 432 to 1342; in one row of 4096 these take
+// 47, 21, 38 and 604. The second pass shares the first one's registers: of the
+// fp16 kernels `tile` spills 8 a lane for it, `mid` of 64 x 64 with one buffer 6.
 //
-// What the forms reach (bf16 unless said; weights from HBM):
-//   split   1 token    x 4096x4096     5.3 us (a launch alone is 2-3)
-//   gemv    4 tokens   x 28672x4096   16 us, 3.9 TB/s
-//   mid     64 tokens  x 4096x4096     9.7 us
+// What the forms reach (bf16 unless said; medians of graph replays, 600 MB of
+// weights in turn, so that they come from HBM and not from the 256 MB cache
+// before it; the choices below were measured with 25 to 310 MB in turn, unless
+// they say otherwise):
+//   split   1 token    x 4096x4096     5.0 us (a launch alone is 2-3)
+//   gemv    4 tokens   x 28672x4096   19 us, 3.3 TB/s
+//   mid     64 tokens  x 4096x4096     9.4 us
 //   mid     256 tokens x 4096x4096    17.8 us, 480 TFLOP/s
-//   tile    2048 tokens x 28672x4096  405 us, 1190 TFLOP/s
-//   mid4    256 tokens x 4096x4096    10.6 us, 810 TFLOP/s
+//   tile    2048 tokens x 28672x4096  395 us, 1220 TFLOP/s
+//   mid4    1 token    x 4096x4096     5.6 us
+//   mid4    4 tokens   x 28672x4096   14.8 us, 4.2 TB/s
+//   mid4    256 tokens x 4096x4096    10.5 us, 820 TFLOP/s
 //   tile4   2048 tokens x 28672x4096  162 us, 2970 TFLOP/s
 #include "mx4.h"
 
@@ -34,9 +44,9 @@ __device__ __forceinline__ void store_tile(TY *Y, int64_t m, int64_t n, int64_t 
 // Up to 16 tokens, 16-bit activations, few rows. Block: 16 rows, the columns
 // split over W waves in items of 128 U, each wave's next item in flight while it
 // multiplies the current one. The waves' sums are added in wave order through
-// LDS. Bound by latency: 4096x4096 is two items a wave (1 token 5.3 us, 16
-// tokens 8.0); with many tokens by the loads of their rows (4096x14336: 1 token
-// 12.4 us, 16 tokens 21.6).
+// LDS. Bound by latency: 4096x4096 is one item a wave, all of it loaded at once
+// and nothing in flight behind it (1 token 5.0 us, 16 tokens 7.8); with many
+// tokens by the loads of their rows (4096x14336: 1 token 13.6 us, 16 tokens 23.0).
 template <typename TX, typename TY, int U, int W>
 __global__ __launch_bounds__(64 * W) void k_mx4_gemm_split(const TX *__restrict__ X, int M, int nb,
                                                            const uint8_t *__restrict__ codes,
@@ -74,8 +84,10 @@ hipError_t split(const TX *X, int M, int nb, const uint8_t *codes, const uint8_t
 // units for a whole block each. Block: 8 / S row tiles of 16, all columns, S
 // waves a tile; the activations go through LDS in chunks of kc blocks that all
 // waves share. Every wave streams its own weights (see StreamItem), the next
-// item in flight also across the chunks' barriers. Bound by HBM: 28672x4096 (62
-// MB) 16 us, 3.9 TB/s, where a plain read of as much reaches 6.
+// item in flight also across the chunks' barriers. Bound by how much the waves
+// have in flight: 4 tokens x 28672x4096 (62 MB from HBM) 19 us, 3.3 TB/s, where a
+// plain read of as much takes 11.6 us, 5.6 TB/s; with the weights partly in the
+// last-level cache 16 us.
 template <typename TX, typename TY, int S>
 __global__ __launch_bounds__(512, 4) void k_mx4_gemv(const TX *__restrict__ X, int M, int nb, int kc,
                                                      const uint8_t *__restrict__ codes,
@@ -249,8 +261,10 @@ __device__ __forceinline__ u32x2 load_scales8(const uint8_t *row, int b0, int nb
 }
 
 // The products below stage both operands through LDS, rows of eight 16-byte
-// chunks, chunk q of row m at position q ^ (m & 7): the eight rows that one
-// 128-byte LDS cycle serves then lie on distinct banks. A load unit takes 64
+// chunks, chunk q of row m at position q ^ (m & 7): equal chunks of eight
+// consecutive rows then lie on distinct banks of 32. Conflicts remain, 0.16 to 0.37
+// cycles for every busy LDS cycle (2048 tokens x 28672x4096: 0.37 `tile`, 0.33
+// `tile4`); where they come from has not been measured. A load unit takes 64
 // cycles for a load whose neighbouring lanes lie in different rows, as a matrix
 // operand wants them, whatever its width, and 19 where eight lanes cover 128
 // bytes (measured): weights read straight into operand registers, and scales a
@@ -263,9 +277,9 @@ __device__ __forceinline__ int swizzled(int row, int q) { return row * 8 + (q ^ 
 // use. What comes next is on its way to registers meanwhile; activations have
 // two buffers, so a step costs one barrier, and a fourth one more. Weights are
 // converted by the wave that multiplies them (no other one has its rows), once
-// for 128 tokens. 2048 tokens x 28672x4096: 405 us, 1190 TFLOP/s (8192 tokens:
-// 1230), the matrix units busy for 56 % of it; a dense bf16 library product of
-// the shape takes 398 us.
+// for 128 tokens. 2048 tokens x 28672x4096: 395 us, 1220 TFLOP/s (8192 tokens:
+// 1260), the matrix units busy for 57 % of it, LDS for 46 %; a dense bf16 library
+// product of the shape takes 368 us.
 // Lane (r, h) = (lane % 32, lane / 32) of a 32-row tile holds in k-step s of 4
 // columns 32 h + 8 s ... of the step: chunk 4 h + s of an activation row, word
 // s of block h of a weight row.
@@ -487,7 +501,7 @@ __device__ __forceinline__ void add_groups(float (&red)[G / 2][32 * MT][256 / G]
 // LDS buffers: two need one barrier a round, one leaves room for a second block.
 // A round's loads and its LDS accesses, about 500 cycles each for 32 x 64, are
 // what bounds it, and waits where they do not overlap (203 tokens x 4097x4064
-// 19.7 us, 343 TFLOP/s; 64 tokens x 4096x14336 23 us).
+// 21 us, 320 TFLOP/s; 64 tokens x 4096x14336 27 us).
 template <typename TX, typename TY, int MT, int G, int BUF>
 __global__ __launch_bounds__(512, BUF == 2 && MT * G == 8 ? 2 : 4) void k_mx4_gemm_mid(
     const TX *__restrict__ X, int64_t M, int nb, const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales,
@@ -809,9 +823,11 @@ __global__ __launch_bounds__(512, 2) void k_mx4_gemm_tile4(const uint8_t *__rest
 // MXFP4 activations, too few 256 x 256 tiles for the chip, or few tokens. Block:
 // 32 MT tokens x 256 / G rows, 8 waves: G groups of 32 rows a wave. A round is
 // 256 G columns, of which each group takes 256; the groups' sums meet in LDS.
-// 256 tokens x 4096x4096 10.6 us (four rounds: latency), 256 tokens x 4096x14336
-// 28.7 us, 1050 TFLOP/s: bound by a round's loads and LDS accesses one after the
-// other. (A second buffer and loads two rounds ahead: 11.1 and 27.1 us.)
+// 256 tokens x 4096x4096 10.5 us (four rounds: latency), 256 tokens x 4096x14336
+// 35 us, 855 TFLOP/s (28.7 with the weights in the last-level cache): bound by a
+// round's loads and LDS accesses one after the other. (A second buffer and loads
+// two rounds ahead: 11.1 and, from the cache, 27.1 us.) Up to 16 tokens too, by
+// tiles of 32 (1 and 16 tokens: 4096x4096 5.6 and 5.8 us, 28672x4096 14.7 and 15.8).
 template <typename TY, int MT, int G>
 __global__ __launch_bounds__(512, 4) void k_mx4_gemm_mid4(const uint8_t *__restrict__ xcodes,
                                                           const uint8_t *__restrict__ xscales, int64_t M, int nb,
@@ -959,10 +975,14 @@ hipError_t gemm(const TX *X, int64_t M, int nb, const uint8_t *codes, const uint
 {
     if (M <= 16) {
         // Enough row tiles for more than a block's worth a unit: few waves a
-        // tile (28672 rows of 4096, 4 tokens: S = 1, 2, 4, 8 take 16.4, 15.7,
-        // 17.9, 21.1 us; 12288 rows, 2 tokens: 14.4, 10.3, 9.7, 10.9). Above 16
-        // tokens `mid`: with 16 x 28672x4096 it takes 22 us, gemv 19; with 16 x
-        // 4096x14336 19, split 21.6, but 8 tokens 17.2 both, 1 token 16.8, 12.4.
+        // tile (600 MB in turn, 4 tokens, gemv with S = 1, 2, 4, 8, then split, us:
+        // 28672 rows of 4096 20.4, 17.7, 20.7, 25.2, 33.1; 12288 rows 18.6, 12.7,
+        // 11.3, 12.9, 15.4). Fewer rows: split (4096x4096, 1, 4, 16 tokens 5.0, 5.8,
+        // 7.8, gemv with S = 8 6.5, 6.7, 10.3; 4096x14336 13.5, 15.4, 22.6, gemv 19.8,
+        // 20.7, 37.9). Above 16 tokens `mid`, whose time hardly depends on the
+        // tokens: 4096x4096 8.7, 4096x14336 25.5, 28672x4096 20.9 at 16 tokens, gemv
+        // 20.1. In between it is not the best everywhere: 8192x4096, from 4 tokens on
+        // split takes 10.8 to 14.9 where `mid` takes 10.0 and gemv, to 8 tokens, 9.5.
         const int64_t tiles = tiles_of(out, 16);
         if (tiles >= 1280)
             return gemv<TX, TY, 2>(X, (int)M, nb, codes, scales, out, Y, st);

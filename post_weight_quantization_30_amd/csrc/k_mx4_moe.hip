@@ -12,13 +12,15 @@
 // of routed experts is found by every block from the routing's ids (at most 64 x
 // 16 of them).
 //
-//   1 token, 8 of 64 experts of 2048x1024     24.5 us (27 MB): logits 2.6, up
-//                                             12.3 with the routing, down 9.6
-//   8 tokens, 2 of 8 of 4096x14336            160 us (748 MB, 4.7 TB/s): up 100
-//                                             (5.0 TB/s), down 57 (4.4)
-//   33 tokens, 4 of 48 of 1056x1408           57 us (114 MB): logits 3.2, routing
-//                                             2.6, up 27, down 20, sum 4
-//   1 token, 8 of 256 of 4096x512             24 us
+//   1 token, 8 of 64 experts of 2048x1024     26.5 us (27 MB): logits 2.7, up
+//                                             14.0 with the routing, down 10.3
+//   8 tokens, 2 of 8 of 4096x14336, 7 hit     170 us (655 MB, 3.8 TB/s): up 102
+//                                             (4.3 TB/s), down 58 (3.8)
+//   33 tokens, 4 of 48 of 1056x1408, 44 hit   61 us (105 MB): logits 4.0, routing
+//                                             3.6, up 31, down 20, sum 4.7
+//   1 token, 8 of 256 of 4096x512             26 us
+// (medians, the layers as graph replays, the launches from a kernel trace; experts
+// of 600 MB and more in turn.)
 #include "mx4.h"
 
 namespace awq {
@@ -31,7 +33,7 @@ constexpr int kMaxTok = AWQ_MX4_MOE_MAX_TOKENS, kMaxK = AWQ_MX4_MOE_MAX_TOPK, kM
 // Logits: a block per expert and TOK tokens, its four waves and their lanes
 // along the columns. (A router row is read in whole kilobytes: 16 rows of 64
 // bytes, as a matrix tile would read them, keep a load unit busy twice as long.)
-// Bound by latency: 2.6 us for 1 token, 64 experts of 2048 columns; one block
+// Bound by latency: 2.7 us for 1 token, 64 experts of 2048 columns; one block
 // for all experts of 16 tokens took 11.
 template <typename TX, int TOK>
 __global__ __launch_bounds__(256) void k_mx4_moe_logits(const TX *__restrict__ X, int M, int hidden,
@@ -253,9 +255,11 @@ __device__ __forceinline__ void read_routing(Routed &rt, const int32_t *ids, int
 // hidden columns. The tokens' activations lie in LDS by chunks of kc blocks;
 // every wave streams its weights (see StreamItem). ROUTE: every block routes all
 // tokens, a wave each, from the logits, and the first leaves `ids` for `down`.
-// 8 tokens x 8 experts of 4096x14336: 100 us, 499 MB at 5.0 TB/s. Small experts
+// 8 tokens, 7 experts of 4096x14336: 102 us, 437 MB at 4.3 TB/s. Small experts
 // lose by their starts: a block reads routing, tokens and first weights one
-// after another (33 tokens, 48 experts of 1056x1408: 27 us, 76 MB at 2.8 TB/s).
+// after another (33 tokens, 44 experts of 1056x1408: 31 us, 70 MB at 2.3 TB/s).
+// The fp16 form spills 7 to 8 registers a lane (its second pass, as in the
+// products: one block below 2^-11 in one row of 64 takes that layer from 64 to 96 us).
 constexpr int kUpWaves = 8;
 
 template <typename TX, int S, bool ROUTE>
@@ -371,7 +375,10 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void k_mx4_moe_up(const TX *__res
                 const int pair = list[4 * c + k];
                 const float gate = acc[0][0][k], up = acc[0][1][k];
                 const float v = gate / (1.0f + expf(-gate)) * up * (ROUTE ? own_weights : weights)[pair];
-                // two bf16 parts: 16 significant bits (an infinity stays in the first)
+                // Two bf16 parts: 16 significant bits (an infinity stays in the first).
+                // Of Y that costs 5e-6 (2-norm, 8 tokens, 2 of 8 experts of
+                // 4096x14336), a three-hundredth of a bf16 Y's rounding; a third
+                // part would be half as much again to read and multiply in `down`.
                 const float hi = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, v) & 0xFFFF0000u);
                 bf16 *const out = h + (int64_t)pair * 2 * inter + col0 + r;
                 out[0] = static_cast<bf16>(hi);
@@ -400,7 +407,7 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void k_mx4_moe_up(const TX *__res
 //   wide: 16 hidden columns a wave, each wave all units: the staged rows serve
 //     all waves, which is what counts once tokens have more bytes than weights
 //     (64 tokens x 8 experts of 4096x14336: 332 us narrow, 100 wide).
-// 8 tokens x 8 experts of 4096x14336: 57 us, 249 MB at 4.4 TB/s.
+// 8 tokens, 7 experts of 4096x14336: 58 us, 218 MB at 3.8 TB/s.
 constexpr int kPartBytes = 64 * kStreamBlocks, kRowBytes = 2 * kPartBytes + 16;    // in LDS, padded (see stream_chunk)
 
 // Rows in unit order: group g's begin at per * begin[g], unit i's at + i *
