@@ -310,3 +310,91 @@ def test_moe_byte_254_stays_with_its_tokens(awq):
     hit = (ids == 3).any(1)
     assert hit.any() and not hit.all()
     assert not np.isfinite(Y[hit]).any() and np.isfinite(Y[~hit]).all()
+
+
+# ---- long operands ----------------------------------------------------------------
+
+
+def codes_on_gpu(rows, n, seed, lo=119, hi=122):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    c = torch.randint(0, 256, (*rows, n // 2), dtype=torch.uint8, device="cuda", generator=g)
+    return c, torch.randint(lo, hi, (*rows, n // 32), dtype=torch.uint8, device="cuda", generator=g)
+
+
+@pytest.mark.parametrize("rows,n", [(262141, 32), (300001, 64), (65535 * 4 + 4, 288)])
+def test_quantize_with_s_of_many_rows(awq, rows, n):
+    """More rows than the grid has blocks of four for."""
+    say("quantize many rows", rows, n)
+    r = np.random.default_rng(41)
+    W, W32 = store(r.standard_normal((rows, n)), "bf16")
+    s = np.exp(r.uniform(-1.5, 1.5, n)).astype(np.float32)
+    c, sc = awq.mx4_quantize(W, s=torch.from_numpy(s).cuda())
+    pick = np.r_[0:2000, rows // 2:rows // 2 + 2000, rows - 2000:rows]
+    want_c, want_s = mx.quantize(W32[pick], s)
+    at = torch.from_numpy(pick).cuda()
+    assert np.array_equal(host(c[at]), want_c) and np.array_equal(host(sc[at]), want_s)
+    again, sc2 = awq.mx4_quantize(W * torch.from_numpy(s).cuda())      # fp32 products, no s
+    assert torch.equal(c, again) and torch.equal(sc, sc2)
+
+
+@pytest.mark.parametrize("with_s", [False, True])
+def test_quantize_and_back_beyond_32_bits(awq, with_s):
+    rows, n = 1040500, 4128                                # 2^32 values and more
+    say("quantize long", rows, n, with_s)
+    W = torch.empty(rows, n, dtype=torch.bfloat16, device="cuda")
+    W.normal_(generator=torch.Generator(device="cuda").manual_seed(5))
+    s = torch.rand(n, device="cuda") + 0.5 if with_s else None
+    c, sc = awq.mx4_quantize(W, s=s)
+    v = awq.mx4_dequantize(c, sc)
+    for at in (slice(0, 50), slice(rows // 2 - 25, rows // 2 + 25), slice(rows - 50, rows)):
+        want_c, want_s = mx.quantize(host(W[at].float()), None if s is None else host(s))
+        assert np.array_equal(host(c[at]), want_c) and np.array_equal(host(sc[at]), want_s)
+        assert np.array_equal(host(v[at].double()), mx.dequantize(want_c, want_s))
+
+
+@pytest.mark.parametrize("M", [1, 5, 40])
+def test_products_of_weights_beyond_32_bits(awq, M):
+    out, n = 2080900, 4128                                 # 4.3 GB of codes
+    say("long weights", M, out, n)
+    c, s = codes_on_gpu((out,), n, 6)
+    X, X32 = store(np.random.default_rng(42).standard_normal((M, n)), "bf16")
+    xc, xs = awq.mx4_quantize(X)
+    Y, Y4 = awq.mx4_gemm(X, c, s, y_f32=True), awq.mx4_gemm_a4(xc, xs, c, s, dtype=torch.float32)
+    for at in (slice(0, 70), slice(out // 2, out // 2 + 70), slice(out - 70, out)):
+        Wd = mx.dequantize(host(c[at]), host(s[at]))
+        assert (far(Y[:, at], *product(X32, Wd), n) <= 1).all()
+        assert (far(Y4[:, at], *product(mx.dequantize(host(xc), host(xs)), Wd), n) <= 1).all()
+
+
+def test_products_of_activations_beyond_32_bits(awq):
+    M, out, n = 2097120, 70, 4128                          # as many tokens as a call takes
+    say("long activations", M, out, n)
+    X = torch.empty(M, n, dtype=torch.bfloat16, device="cuda")
+    X.normal_(generator=torch.Generator(device="cuda").manual_seed(7))
+    c, s = codes_on_gpu((out,), n, 8)
+    xc, xs = awq.mx4_quantize(X)
+    Y, Y4 = awq.mx4_gemm(X, c, s, y_f32=True), awq.mx4_gemm_a4(xc, xs, c, s, dtype=torch.float32)
+    Wd = mx.dequantize(host(c), host(s))
+    for at in (slice(0, 150), slice(M // 2, M // 2 + 150), slice(M - 150, M)):
+        assert (far(Y[at], *product(host(X[at].float()), Wd), n) <= 1).all()
+        assert (far(Y4[at], *product(mx.dequantize(host(xc[at]), host(xs[at])), Wd), n) <= 1).all()
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("M", [1, 20])
+def test_moe_weights_beyond_32_bits(awq, M, dt):
+    """256 experts of 4.3 GB of gate and up codes; the last three alone have positive logits."""
+    E, k, hidden, inter = 256, 2, 16416, 1024
+    say("moe long", M, dt)
+    r = np.random.default_rng(43)
+    w = (*codes_on_gpu((E, 2 * inter), hidden, 9), *codes_on_gpu((E, hidden), inter, 10))
+    X, X32 = store(np.abs(r.standard_normal((M, hidden))) * 0.25, dt)
+    router = np.zeros((E, hidden))
+    router[-3:] = np.abs(r.standard_normal((3, hidden))) * 4 / hidden
+    R, R32 = store(router, dt)
+    Y = awq.mx4_moe(X, R, *w, k).float().cpu().numpy()
+    last = [host(t[-3:]) for t in w]
+    refs = [moe_reference(X32, R32[-3:], *last, ids, True, dt) for ids in moe_routings(X32, R32[-3:], k)]
+    worst = np.min([(np.abs(Y - want) / bound).max(1) for want, bound in refs], axis=0)
+    say("max err/bound", float(worst.max()))
+    assert (worst <= 1).all()
