@@ -390,7 +390,7 @@ int awq_mx4_gemm_a4(const uint8_t *xcodes, const uint8_t *xscales, int64_t M, in
  * each token x (a row of X):
  *   l = router x (fp32); the top_k experts with the largest l (equal ones: the
  *   lowest index; a NaN ranks lowest); p = softmax(l) over all experts at those,
- *   divided by their sum if renorm is not 0;
+ *   divided by their sum if renorm is not 0 (without it a NaN among l makes p NaN);
  *   h_e = silu(Wgate_e x) * (Wup_e x);  y = sum_e p_e Wdown_e h_e.
  * Everything is fp32 up to Y (the products with the experts as above) but p_e h_e,
  * which keeps 16 significant bits (and fp32's range).

@@ -312,6 +312,20 @@ def test_moe_byte_254_stays_with_its_tokens(awq):
     assert not np.isfinite(Y[hit]).any() and np.isfinite(Y[~hit]).all()
 
 
+@pytest.mark.parametrize("M", [3, 20])
+def test_moe_nan_logit_without_renorm(awq, M):
+    """A NaN among a token's logits: its softmax is NaN; renormalised weights leave it out."""
+    say("moe nan logit", M)
+    E, k, hidden, inter = 6, 2, 96, 64
+    r = np.random.default_rng(36)
+    w = dev(*experts(r, E, hidden, inter))
+    X, X32 = store(r.standard_normal((M, hidden)), "f16")
+    R, _ = store(r.standard_normal((E, hidden)) * 1.5 / hidden ** 0.5, "f16")
+    R[4, 7] = NAN
+    assert bool(awq.mx4_moe(X, R, *w, k, renorm=False).isnan().all())
+    assert bool(awq.mx4_moe(X, R, *w, k, renorm=True).isfinite().all())
+
+
 # ---- long operands ----------------------------------------------------------------
 
 
