@@ -664,8 +664,8 @@ hipError_t moe(const void *X, int M, int hidden, int inter, int E, int top_k, in
     // least (microseconds of a whole layer for S = 1, 2, 4, 8: 33 tokens, 4 of 48
     // experts of 1056x1408, 4928 tiles 60.9, 64.5, 71.2, 89.4; 16 tokens, 8 of 64 of
     // 2048x1024, 4096 tiles 65.3, 67.2, 74.5, 87.1; 2 tokens, 2 of 8 of 4096x14336,
-    // 3584 tiles 99.7, 94.1, 98.6, 119; 4 tokens, 8 of 128 of 4096x1536, 3072 tiles
-    // 96.5, 88.1, 91.7, 119; 1 token, 8 of 64 of 2048x1024, 512 tiles 30.7, 26.1,
+    // 3584 tiles 99.7, 94.1, 98.6, 119; 4 tokens, 8 of 128 of 4096x1536, somewhat
+    // fewer 96.5, 88.1, 91.7, 119; 1 token, 8 of 64 of 2048x1024, 512 tiles 30.7, 26.1,
     // 24.1, 24.1: waves beyond the items of 512 columns cost nothing there).
     const int64_t tiles = (int64_t)(inter / 16) * most;
     const int S = tiles >= 2048 && hidden < 4096 ? 1 : tiles >= 1536 ? 2 : tiles >= 768 ? 4 : 8;
