@@ -371,9 +371,9 @@ int awq_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows
  * each output is within (in + 16) * (2^-24 * S + 2^-149) of the exact value (the
  * second term is fp32's smallest step: products and sums may be subnormal), plus
  * the rounding to a 16-bit Y. In S an operand that is subnormal in its 16-bit type
- * (X below 2^-14 in fp16, X or W below 2^-126 in bf16) counts as the smallest normal
- * number: the matrix cores align its products as if it were that large. A row of X or W that holds a NaN makes its own
- * outputs NaN and no others.
+ * (X below 2^-14 in fp16, X or W below 2^-126 in bf16) counts as the smallest
+ * normal number: the matrix cores align its products as if it were that large.
+ * A row of X or W that holds a NaN makes its own outputs NaN and no others.
  * awq_mx4_gemm takes values below 2^128: scale byte 253 stands under magnitudes up
  * to 3 and byte 254 under magnitudes up to 1.5 (awq_mx4_quantize writes neither
  * byte). A larger value, which no 16-bit or fp32 number holds, makes the outputs

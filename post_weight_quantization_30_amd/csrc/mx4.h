@@ -365,8 +365,8 @@ __device__ __forceinline__ void stream_compute(StreamItem<NT> &it, const TX *con
 
 // LDS for activations: rows of kc blocks, padded by 16 bytes (eight rows' pieces
 // of 16 bytes then lie on distinct banks of 32; the counters still show 0.3 to
-// 0.4 conflict cycles a busy one), kStreamLds bytes without the padding. kc for `rows` rows (64 at most): a whole number
-// of items, all columns at most.
+// 0.4 conflict cycles a busy one), kStreamLds bytes without the padding. kc for
+// `rows` rows (64 at most): a whole number of items, all columns at most.
 constexpr int kStreamLds = 64 * 1024;
 __host__ __device__ inline int stream_chunk(int rows, int nb)
 {
