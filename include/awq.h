@@ -504,8 +504,10 @@ int awq_moe_route(const void *logits, int dtype, int64_t M, int experts, const f
  * of tokens. For each token x (a row of X) with its choices e_j and weights w_j:
  *   h_j = silu(Wgate_e x) * (Wup_e x), e = e_j, rounded as awq_mx8_quantize does;
  *   y = sum_j w_j (Wdown_e h_j), in the order of j.
- * Sums are fp32 (the products as in awq_mx4_gemm_a8), h as above and Y are the only
- * roundings to fewer bits. Choices outside [0, experts) are left out (a token without
+ * Sums are fp32. Those of gate and up take their products whole, whatever M and y_dtype
+ * are (the order of the sums goes with M, and with it an h at a border of its 8 bits);
+ * those of down are as in awq_mx4_gemm_a8. h as above and Y are the only roundings to
+ * fewer bits. Choices outside [0, experts) are left out (a token without
  * any others gets zeros); an expert that a token names twice counts twice.
  *   xcodes, xscales: device, the MXFP8 matrix (M, hidden).
  *   ids, weights:    device int32 and fp32 (M, top_k), e.g. of awq_moe_route.

@@ -10,7 +10,7 @@
 // experts, go unsorted, in two launches.
 // (us: 1 token, 8 of 64 experts of 2048x1024 17; 8, 2 of 8 of 4096x14336 164, bound by the
 // weights of the seven that are hit, 4.0 TB/s; 203, 4 of 48 of 1056x1408 69: sort 5, up 39,
-// down 20, sum 5; 2048, 8 of 64 of 2048x1024 200: sort 11, up 95, down 63, sum 28 for 134 MB
+// down 20, sum 5; 2048, 8 of 64 of 2048x1024 276: sort 11, up 174, down 63, sum 28 for 134 MB
 // of fp32 each way.)
 #include "mx8_stream.h"
 #include "mx8_tile.h"
@@ -189,7 +189,11 @@ __device__ __forceinline__ void store_h(const f32x16 &gate, const f32x16 &up, in
 // ---- many pairs an expert: large tiles (see mx8_tile.h) --------------------------------
 
 // A tile of pairs x 128 columns of h: wave tiles of 32 gate rows and their 32 up rows.
-template <bool EXACT, int MT>
+// Products of eight columns exactly, as in k_experts_up: h is the same whatever the number of
+// pairs and the type of Y. (What the matrix cores cut off would move an h next to a border
+// to another 8-bit value, and all of an h where large products cancel: 2-norm of the error of Y
+// 4.8e-4 where fp16's own is 2.1e-4, 1.8e-3 beside bf16's 1.7e-3.)
+template <int MT>
 __device__ __forceinline__ void up_tile(Tile8<MT> &lds, const int4 &t, int c0, const uint8_t *xc, const uint8_t *xs,
                                         int top_k, int nb, int inter, const int32_t *list, const uint8_t *gu,
                                         const uint8_t *gus, uint8_t *hc, uint8_t *hs)
@@ -213,7 +217,7 @@ __device__ __forceinline__ void up_tile(Tile8<MT> &lds, const int4 &t, int c0, c
     const uint8_t *const sp = tid < BM ? xs + xrow(tid) * nb : gus + (w0 + wrow((tid - BM) & 255)) * nb;
     const bool words = (((uintptr_t)xs | (uintptr_t)gus | (uintptr_t)nb) & 3) == 0;
     f32x16 acc[MT][2];
-    tile8_contract<true, EXACT, MT>(lds, acc, xc, xo, gu + w0 * nb * 16, wo, sp, words, nb);
+    tile8_contract<true, true, MT>(lds, acc, xc, xo, gu + w0 * nb * 16, wo, sp, words, nb);
     const int r = lane & 31, h = lane >> 5, col = c0 + 32 * (wave & 3);
     if (col >= inter)
         return;
@@ -225,7 +229,6 @@ __device__ __forceinline__ void up_tile(Tile8<MT> &lds, const int4 &t, int c0, c
     }
 }
 
-template <bool EXACT>
 __global__ __launch_bounds__(512, 2) void k_experts_up_tile(const uint8_t *__restrict__ xc,
                                                             const uint8_t *__restrict__ xs, int top_k, int nb,
                                                             int inter, const int32_t *__restrict__ list,
@@ -241,9 +244,9 @@ __global__ __launch_bounds__(512, 2) void k_experts_up_tile(const uint8_t *__res
         return;
     const int4 t = read_tile(tiles, ti);
     if (t.z > 128)
-        up_tile<EXACT, 4>(lds.four, t, ci * 128, xc, xs, top_k, nb, inter, list, gu, gus, hc, hs);
+        up_tile<4>(lds.four, t, ci * 128, xc, xs, top_k, nb, inter, list, gu, gus, hc, hs);
     else
-        up_tile<EXACT, 2>(lds.two, t, ci * 128, xc, xs, top_k, nb, inter, list, gu, gus, hc, hs);
+        up_tile<2>(lds.two, t, ci * 128, xc, xs, top_k, nb, inter, list, gu, gus, hc, hs);
 }
 
 // A tile of pairs x 256 rows of down.
@@ -549,24 +552,15 @@ hipError_t launch_mx4_experts(const uint8_t *xc, const uint8_t *xs, int64_t M, i
             down((bf16 *)Y);
         return hipGetLastError();
     }
-    // Large tiles from 24 pairs an expert on (8 of 64 experts of 2048x1024, us by tiles and by
-    // streams: 64 tokens, 8 pairs an expert, 81, 77; 100 tokens 81, 97; 200 tokens 85, 112; 4
-    // of 48 of 1056x1408, 17 pairs an expert, 93, 69)
+    // Large tiles from 24 pairs an expert on (us by tiles and by streams, 8 of 64 experts of
+    // 2048x1024: 64 tokens, 8 pairs an expert, 102, 78; 100 tokens 103, 83; 150 tokens, 19 pairs,
+    // 104, 98; 200 tokens, 25 pairs, 105, 112; 300 tokens 104, 142; 4 of 48 of 1056x1408, which
+    // would rather have it later: 17 pairs an expert 104, 69; 25 pairs 105, 83; 33 pairs 106, 94)
     if (pairs >= 24 * (int64_t)experts) {
         const int64_t most = pairs / 256 + hit;
         k_experts_sort<true><<<1, 1024, 0, st>>>(ids, pairs, experts, list, place, count, tiles);
-        // An h that the matrix cores' cut has moved across a border of its 8 bits shows in an
-        // fp16 or fp32 result (2-norm of the error 4.8e-4 where fp16's own is 2.1e-4), not in a
-        // bf16 one (1.8e-3, 1.7e-3). 2048 tokens, 8 of 64 experts of 2048x1024: 285 us in
-        // two parts, 200 in one.
-        auto up = [&](auto exact) {
-            k_experts_up_tile<exact.value><<<experts_grid<4>(most, tiles_of(inter, 128)), 512, 0, st>>>(
-                xc, xs, top_k, hidden / 32, inter, list, count, tiles, gu, gus, hc, hs);
-        };
-        if (y_dtype == AWQ_BF16)
-            up(std::false_type());
-        else
-            up(std::true_type());
+        k_experts_up_tile<<<experts_grid<4>(most, tiles_of(inter, 128)), 512, 0, st>>>(
+            xc, xs, top_k, hidden / 32, inter, list, count, tiles, gu, gus, hc, hs);
         k_experts_down_tile<<<experts_grid<4>(most, tiles_of(hidden, 256)), 512, 0, st>>>(hc, hs, inter / 32, hidden, count,
                                                                                          tiles, dn, dns, part);
     } else {
