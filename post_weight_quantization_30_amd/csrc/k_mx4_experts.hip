@@ -249,8 +249,9 @@ __global__ __launch_bounds__(512, 2) void k_experts_up_tile(const uint8_t *__res
         up_tile<2>(lds.two, t, ci * 128, xc, xs, top_k, nb, inter, list, gu, gus, hc, hs);
 }
 
-// A tile of pairs x 256 rows of down.
-template <int MT>
+// A tile of pairs x 256 rows of down. EXACT, here and in the other forms of down: products of
+// eight columns exactly too, for an fp32 Y.
+template <bool EXACT, int MT>
 __device__ __forceinline__ void down_tile(Tile8<MT> &lds, const int4 &t, int n0, const uint8_t *hc, const uint8_t *hs,
                                           int nb, int hidden, const uint8_t *dn, const uint8_t *dns, float *part)
 {
@@ -271,11 +272,12 @@ __device__ __forceinline__ void down_tile(Tile8<MT> &lds, const int4 &t, int n0,
     const uint8_t *const sp = tid < BM ? hs + (int64_t)xrow(tid) * nb : dns + (w0 + wrow((tid - BM) & 255)) * nb;
     const bool words = (((uintptr_t)hs | (uintptr_t)dns | (uintptr_t)nb) & 3) == 0;
     f32x16 acc[MT][2];
-    tile8_contract<false, false, MT>(lds, acc, hc, xo, dn + w0 * nb * 16, wo, sp, words, nb);
+    tile8_contract<false, EXACT, MT>(lds, acc, hc, xo, dn + w0 * nb * 16, wo, sp, words, nb);
     store_tiles<float, MT>(part + (int64_t)t.y * hidden, acc, reinterpret_cast<float *>(lds.x) + 2048 * wave,
                            32 * MT * (wave >> 2), n0 + 64 * (wave & 3), t.z, hidden, tid & 63);
 }
 
+template <bool EXACT>
 __global__ __launch_bounds__(512, 2) void k_experts_down_tile(const uint8_t *__restrict__ hc,
                                                               const uint8_t *__restrict__ hs, int nb, int hidden,
                                                               const int32_t *__restrict__ count,
@@ -290,9 +292,9 @@ __global__ __launch_bounds__(512, 2) void k_experts_down_tile(const uint8_t *__r
         return;
     const int4 t = read_tile(tiles, ti);
     if (t.z > 128)
-        down_tile<4>(lds.four, t, ci * 256, hc, hs, nb, hidden, dn, dns, part);
+        down_tile<EXACT, 4>(lds.four, t, ci * 256, hc, hs, nb, hidden, dn, dns, part);
     else
-        down_tile<2>(lds.two, t, ci * 256, hc, hs, nb, hidden, dn, dns, part);
+        down_tile<EXACT, 2>(lds.two, t, ci * 256, hc, hs, nb, hidden, dn, dns, part);
 }
 
 // ---- few pairs an expert: weights as a stream (see mx8_stream.h) --------------------------
@@ -402,6 +404,7 @@ __global__ __launch_bounds__(512, 4) void k_experts_down_direct(const uint8_t *_
                                                                 const uint8_t *__restrict__ dn,
                                                                 const uint8_t *__restrict__ dns, TY *__restrict__ Y)
 {
+    constexpr bool EXACT = std::is_same<TY, float>::value;
     __shared__ float sums[8 * kDirect][17];            // part and pair, row
     __shared__ int own[8][16];
     const int pairs = M * top_k, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -431,10 +434,18 @@ __global__ __launch_bounds__(512, 4) void k_experts_down_direct(const uint8_t *_
                 x1[k] = bx + 8 + k < nb ? *reinterpret_cast<const u32x4 *>(x + (int64_t)(bx + 8 + k) * 32 + 16 * (c & 1)) : zero;
             }
             const uint32_t sx = mx4_scales4(xs, b, nb), sw = mx4_scales4(ws, b, nb);
-            acc = mfma16_a8<0>(join(x0[0], x1[0]), sx, wr[0], sw, acc);
-            acc = mfma16_a8<1>(join(x0[1], x1[1]), sx, wr[1], sw, acc);
-            acc = mfma16_a8<2>(join(x0[2], x1[2]), sx, wr[2], sw, acc);
-            acc = mfma16_a8<3>(join(x0[3], x1[3]), sx, wr[3], sw, acc);
+            auto step = [&]<int U>() {
+                i32x8 high = join(x0[U], x1[U]), low;
+                if constexpr (EXACT)
+                    mx8_parts(join(x0[U], x1[U]), high, low);
+                acc = mfma16_a8<U>(high, sx, wr[U], sw, acc);
+                if constexpr (EXACT)
+                    acc = mfma16_a8<U>(low, sx, wr[U], sw, acc);
+            };
+            step.template operator()<0>();
+            step.template operator()<1>();
+            step.template operator()<2>();
+            step.template operator()<3>();
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -461,7 +472,7 @@ __global__ __launch_bounds__(512, 4) void k_experts_down_direct(const uint8_t *_
 }
 
 // A tile and 128 / S rows of down, S waves a row tile.
-template <int S>
+template <int S, bool EXACT>
 __global__ __launch_bounds__(512, 4) void k_experts_down(const uint8_t *__restrict__ hc, const uint8_t *__restrict__ hs,
                                                          int nb, int hidden, const int32_t *__restrict__ count,
                                                          const int4 *__restrict__ tiles,
@@ -477,7 +488,7 @@ __global__ __launch_bounds__(512, 4) void k_experts_down(const uint8_t *__restri
     const int n0 = ci * (128 / S) + wave / S * 16 + r;
     const int64_t n = (int64_t)t.x * hidden + (n0 < hidden ? n0 : hidden - 1);
     f32x4 acc;
-    stream_contract<false, S>(acc, lds.in, hc, hs, [&](int m) { return t.y + m; }, t.z, dn + n * nb * 16, dns + n * nb,
+    stream_contract<EXACT, S>(acc, lds.in, hc, hs, [&](int m) { return t.y + m; }, t.z, dn + n * nb * 16, dns + n * nb,
                               wave % S, nb);
     __syncthreads();                                   // the waves' sums in wave order
     lds.red[wave][lane] = acc;
@@ -561,8 +572,14 @@ hipError_t launch_mx4_experts(const uint8_t *xc, const uint8_t *xs, int64_t M, i
         k_experts_sort<true><<<1, 1024, 0, st>>>(ids, pairs, experts, list, place, count, tiles);
         k_experts_up_tile<<<experts_grid<4>(most, tiles_of(inter, 128)), 512, 0, st>>>(
             xc, xs, top_k, hidden / 32, inter, list, count, tiles, gu, gus, hc, hs);
-        k_experts_down_tile<<<experts_grid<4>(most, tiles_of(hidden, 256)), 512, 0, st>>>(hc, hs, inter / 32, hidden, count,
-                                                                                         tiles, dn, dns, part);
+        auto down = [&](auto exact) {
+            k_experts_down_tile<exact.value><<<experts_grid<4>(most, tiles_of(hidden, 256)), 512, 0, st>>>(
+                hc, hs, inter / 32, hidden, count, tiles, dn, dns, part);
+        };
+        if (y_dtype == AWQ_F32)
+            down(std::true_type());
+        else
+            down(std::false_type());
     } else {
         const int64_t most = pairs / kSmall + hit;
         k_experts_sort<false><<<1, 1024, 0, st>>>(ids, pairs, experts, list, place, count, tiles);
@@ -570,14 +587,18 @@ hipError_t launch_mx4_experts(const uint8_t *xc, const uint8_t *xs, int64_t M, i
             xc, xs, top_k, hidden / 32, inter, ids, (int)pairs, experts, list, count, tiles, gu, gus, hc, hs);
         // (203 tokens, 4 of 48 experts of 1056x1408, by one, two, four waves a row tile: 71, 69,
         // 70 us a layer; 64, 8 of 64 of 2048x1024 80, 77, 89; 8, 2 of 8 of 4096x14336 162, 167, 140)
-        auto down = [&]<int S>() {
-            k_experts_down<S><<<experts_grid<1>(most, tiles_of(hidden, 128 / S)), 512, 0, st>>>(hc, hs, inter / 32, hidden,
-                                                                                              count, tiles, dn, dns, part);
+        auto down = [&]<int S, bool EXACT>() {
+            k_experts_down<S, EXACT><<<experts_grid<1>(most, tiles_of(hidden, 128 / S)), 512, 0, st>>>(
+                hc, hs, inter / 32, hidden, count, tiles, dn, dns, part);
         };
-        if (inter >= 4096)
-            down.template operator()<4>();
+        if (inter >= 4096 && y_dtype == AWQ_F32)
+            down.template operator()<4, true>();
+        else if (inter >= 4096)
+            down.template operator()<4, false>();
+        else if (y_dtype == AWQ_F32)
+            down.template operator()<2, true>();
         else
-            down.template operator()<2>();
+            down.template operator()<2, false>();
     }
     const uint32_t blocks = (uint32_t)((M * (hidden / 4) + 255) / 256);
     if (y_dtype == AWQ_F32)

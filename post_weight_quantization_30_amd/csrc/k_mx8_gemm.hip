@@ -1,13 +1,17 @@
 // k_mx8_gemm.hip -- products of MXFP8 activations with MXFP4 weights, Y[m][n] = sum_k X[m][k] W[n][k].
 //
 // The scaled matrix instructions take both operands as they are stored, codes and
-// scale bytes, so the only roundings are those of the fp32 sums.
+// scale bytes, so the only roundings are those of the fp32 sums. What the matrix cores cut off
+// products of eight columns (see mx8_stream.h) lies far below a 16-bit Y's rounding, but
+// not below that of an fp32 Y: for that one activations go in two parts.
 #include "mx8_mid.h"
 #include "mx8_stream.h"
 
 namespace awq {
 
 namespace {
+
+template <typename TY> constexpr bool kExact = std::is_same<TY, float>::value;
 
 // Up to 16 tokens (see mx8_stream.h). Block: 8 / S row tiles of 16, S waves a tile. Bound by
 // the weights on their way, 4 KB a wave: 4 tokens x 28672x4096 17.9 us, 3.5 TB/s; small
@@ -23,7 +27,7 @@ __global__ __launch_bounds__(512, 4) void k_mx8_gemm_stream(const uint8_t *__res
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, c = lane >> 4;
     const int64_t n0 = ((int64_t)blockIdx.x * (8 / S) + wave / S) * 16, n = n0 + r < out ? n0 + r : out - 1;
     f32x4 acc;
-    stream_contract<false, S>(acc, lds.in, xcodes, xscales, [](int m) { return m; }, M, codes + n * nb * 16, scales + n * nb, wave % S, nb);
+    stream_contract<kExact<TY>, S>(acc, lds.in, xcodes, xscales, [](int m) { return m; }, M, codes + n * nb * 16, scales + n * nb, wave % S, nb);
     __syncthreads();                                   // the waves' sums in wave order
     lds.red[wave][lane] = acc;
     __syncthreads();
@@ -54,7 +58,7 @@ __global__ __launch_bounds__(kMidThreads) void k_mx8_gemm_mid(const uint8_t *__r
         return;
     m0 *= 32;
     n0 *= 32 * NT;
-    mid8_contract(
+    mid8_contract<kExact<TY>>(
         lds, xcodes + m0 * nb * 32, xscales + m0 * nb, [&](int m) { return m0 + m < M ? m : (int)(M - 1 - m0); },
         codes + n0 * nb * 16, scales + n0 * nb, [&](int n) { return n0 + n < out ? n : (int)(out - 1 - n0); }, nb);
     // wave q: registers 4 q ... of every tile, tokens 8 q + 4 h ...
@@ -94,7 +98,7 @@ __device__ __forceinline__ void tile(Tile8<MT> &lds, int64_t m0, int64_t n0, con
     const uint8_t *const sp = tid < BM ? xscales + xrow(tid) * nb : scales + wrow(tid - BM) * nb;
     const bool words = (((uintptr_t)xscales | (uintptr_t)scales | (uintptr_t)nb) & 3) == 0;
     f32x16 acc[MT][2];
-    tile8_contract<false, false, MT>(lds, acc, xcodes + m0 * nb * 32, xo, codes + n0 * nb * 16, wo, sp, words, nb);
+    tile8_contract<false, kExact<TY>, MT>(lds, acc, xcodes + m0 * nb * 32, xo, codes + n0 * nb * 16, wo, sp, words, nb);
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     store_tiles<TY, MT>(Y, acc, reinterpret_cast<float *>(lds.x) + 2048 * wave, m0 + 32 * MT * (wave >> 2),
                         n0 + 64 * (wave & 3), M, out, tid & 63);
@@ -157,10 +161,13 @@ hipError_t gemm_a8(const uint8_t *xc, const uint8_t *xs, int64_t M, int nb, cons
     }
     // Blocks of 32 x 64, two on a unit at a time, or large tiles: 4096 columns take 15 us for
     // each 512 of the small (256 x 4096 rows 15, tiles 28; 512 x 4096 26, 29; 64 x 28672 35,
-    // 33), 30 for one round of half tiles and 55 for each of whole ones. Small blocks of
+    // 33), 30 for one round of half tiles and 55 for each of whole ones; in two parts, for
+    // which the large tiles' matrix cores need twice as long, 50 and 92 (512 x 4096 small
+    // 30, tiles 50; 1024 x 4096 54, 53; 64 x 28672 38, 54; 128 x 28672 60, 54). Small blocks of
     // 32 x 32 where no unit has more than one (64 x 4096 rows 8.3 us, by 32 x 64 10.8).
+    constexpr int half = kExact<TY> ? 50 : 30, round = kExact<TY> ? 92 : 55;
     const int64_t small = tiles_of(M, 32) * tiles_of(out, 64), large = tiles_of(M, 256) * tiles_of(out, 256);
-    if (15 * tiles_of(small, 512) >= (2 * large <= 256 ? 30 : 55 * tiles_of(large, 256))) {
+    if (15 * tiles_of(small, 512) >= (2 * large <= 256 ? half : round * tiles_of(large, 256))) {
         const int64_t chunk = tiles_of(large, 8), whole = whole_tiles(chunk);
         k_mx8_gemm_tile<TY><<<(uint32_t)(8 * (2 * chunk - whole)), 512, 0, st>>>(xc, xs, M, nb, codes, scales, out, Y);
     } else if (tiles_of(M, 32) * tiles_of(out, 32) <= 256) {

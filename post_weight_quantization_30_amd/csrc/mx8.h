@@ -84,6 +84,16 @@ __device__ __forceinline__ uint32_t mx8_upper(uint32_t v)
     return v & ((m << 8) - m);
 }
 
+// The two parts of an operand whose products of eight columns all fit (see mx8_stream.h).
+__device__ __forceinline__ void mx8_parts(const i32x8 &x, i32x8 &high, i32x8 &low)
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        high[i] = (int)mx8_upper((uint32_t)x[i]);
+        low[i] = x[i] ^ high[i];
+    }
+}
+
 __device__ __forceinline__ i32x8 join(const u32x4 &a, const u32x4 &b)
 {
     return i32x8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};

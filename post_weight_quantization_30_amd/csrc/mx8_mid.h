@@ -6,6 +6,7 @@
 // 128 bytes of every activation row and 64 of every weight row, loaded from memory without
 // registers, and waits for nobody; the waves' sums meet in LDS at the end, in wave order.
 // Scales are staged for 128 blocks of columns at a time by the whole block.
+// EXACT: the activations in the two parts of mx8_stream.h, twice the matrix instructions.
 // LDS places as in mx8_tile.h.
 #pragma once
 
@@ -33,7 +34,7 @@ template <int NT> struct Mid8 {
 // The sums of all waves over the block's tokens and weight rows, in lds.sums[0 ... 3]. xrow(m),
 // wrow(n): row indices, 0 <= m < 32, 0 <= n < 32 NT, every one of rows that exist, within
 // 2^32 bytes of codes. All waves have written theirs when this returns.
-template <int NT, typename XRow, typename WRow>
+template <bool EXACT, int NT, typename XRow, typename WRow>
 __device__ __forceinline__ void mid8_contract(Mid8<NT> &lds, const uint8_t *xc, const uint8_t *xs, XRow xrow,
                                               const uint8_t *wc, const uint8_t *ws, WRow wrow, int nb)
 {
@@ -97,9 +98,16 @@ __device__ __forceinline__ void mid8_contract(Mid8<NT> &lds, const uint8_t *xc, 
         const u32x4 *const row = &in.x[r * 8];
         const int swz = r >> 1 & 7;
         const i32x8 x = join(row[(4 * S + h) ^ swz], row[(4 * S + 2 + h) ^ swz]);
+        i32x8 high = x, low;
+        if constexpr (EXACT)
+            mx8_parts(x, high, low);
 #pragma unroll
-        for (int b = 0; b < NT; ++b)
-            acc[b] = mfma32_a8<false, 2 * S>(x, sx, in.w[(32 * b + r) * 4 + ((2 * S + h) ^ (r >> 2 & 3))], sw[b], acc[b]);
+        for (int b = 0; b < NT; ++b) {
+            const u32x4 w = in.w[(32 * b + r) * 4 + ((2 * S + h) ^ (r >> 2 & 3))];
+            acc[b] = mfma32_a8<false, 2 * S>(high, sx, w, sw[b], acc[b]);
+            if constexpr (EXACT)
+                acc[b] = mfma32_a8<false, 2 * S>(low, sx, w, sw[b], acc[b]);
+        }
     };
     // Stages of one chunk of scales: k = first ... end - 1, the wave's own among them; what is
     // loaded ahead may lie in the next chunk.

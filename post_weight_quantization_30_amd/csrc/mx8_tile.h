@@ -205,11 +205,7 @@ __device__ __forceinline__ void tile8_contract(Tile8<MT> &lds, f32x16 (&acc)[MT]
             for (int b = 0; b < 2; ++b)
                 if constexpr (EXACT) {
                     i32x8 high, low;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        high[i] = (int)mx8_upper((uint32_t)x[a][i]);
-                        low[i] = x[a][i] ^ high[i];
-                    }
+                    mx8_parts(x[a], high, low);
                     acc[a][b] = mfma32_a8<TURNED, 2 * S>(high, sx[a], w[b], sw[b], acc[a][b]);
                     acc[a][b] = mfma32_a8<TURNED, 2 * S>(low, sx[a], w[b], sw[b], acc[a][b]);
                 } else {

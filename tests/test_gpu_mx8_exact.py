@@ -1,10 +1,13 @@
-"""The routed experts on operands whose fp32 sums are exact (mx8_exact.py): h bit for bit and the
-results of down within its own bound, by every way that a call can take.
+"""Products with MXFP8 activations and the routed experts on operands whose fp32 sums are exact
+(mx8_exact.py): results and the experts' h bit for bit, by every way that a call can take.
 Each test prints the case it runs (flushed) before touching the GPU.
 """
+import numpy as np
 import pytest
+import torch
 
 import mx8_exact as ex
+from oracle import mx4_oracle as mx4, mx8_oracle as mx
 from test_gpu_mx4 import DT, awq, say  # noqa: F401
 from test_gpu_mx8 import dev
 
@@ -24,7 +27,7 @@ def test_experts_h(awq, case, dt):
     assert off <= 1
 
 
-@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
 @pytest.mark.parametrize("case", range(len(ex.LAYERS)))
 def test_experts_sums(awq, case, dt):
     say("experts' sums", *ex.LAYERS[case], dt)
@@ -33,3 +36,33 @@ def test_experts_sums(awq, case, dt):
     off = layer.check(Y.cpu().double().numpy(), dt, ex.some_tokens(layer.shape[0], 8))
     say("err/bound", off)
     assert off <= 1
+
+
+# M, out, in: up to 16 tokens by two, four, eight waves a row tile; small tiles; large ones, whole and half
+GEMM = [(1, 70, 32), (1, 300, 4096), (4, 20490, 160), (16, 10250, 608), (15, 1000, 14336), (17, 130, 1024), (33, 65, 32),
+        (70, 500, 2080), (40, 2000, 4128), (128, 4100, 160), (250, 4090, 1184), (1000, 700, 1056), (2050, 4097, 256), (2050, 4097, 1312)]
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("M,out,n", GEMM)
+def test_gemm_a8(awq, M, out, n, dt):
+    """Without large products nothing is cut off: the exact sums, rounded to Y's type."""
+    say("gemm_a8, exact sums", M, out, n, dt)
+    r = np.random.default_rng(M + n)
+    xc, xs = ex.tokens(r, M, n, 0)
+    c, s = ex.rows(r, (out,), n)
+    Y = awq.mx4_gemm_a8(*dev(xc, xs, c, s), dtype=DT[dt]).cpu()
+    want = torch.from_numpy(ex.sums(mx.dequantize(xc, xs), mx4.dequantize(c, s))).to(DT[dt])
+    assert torch.equal(Y, want)
+
+
+@pytest.mark.parametrize("M,out,n", GEMM)
+def test_gemm_a8_fp32_keeps_small_products_beside_large(awq, M, out, n):
+    say("gemm_a8, fp32, large products", M, out, n)
+    r = np.random.default_rng(M + n)
+    xc, xs = ex.tokens(r, M, n)
+    c, s = ex.rows(r, (out,), n)
+    Y = awq.mx4_gemm_a8(*dev(xc, xs, c, s), dtype=torch.float32).cpu()
+    want = torch.from_numpy(ex.sums(mx.dequantize(xc, xs), mx4.dequantize(c, s))).float()
+    say("wrong", float((Y != want).float().mean()))
+    assert torch.equal(Y, want)
