@@ -57,15 +57,15 @@ static __device__ const u32x4 kTile8Zeros = {0, 0, 0, 0};
 
 // 16 bytes a lane from memory to LDS, lane i's to `to` + 16 i, without registers on the
 // way. In flight until a wait for the vector memory counter that the compiler knows
-// nothing of: those are written out below.
+// nothing of: those are written out below. The LDS address goes in m0, as an operand: the
+// compiler sets it, and knows what the register holds. (One wait state between the two.)
 __device__ __forceinline__ void load_to_lds(const uint8_t *from, uint32_t to)
 {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(to) : "memory");
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "{m0}"(to) : "memory");
 }
 __device__ __forceinline__ void load_to_lds(const uint8_t *base, uint32_t off, uint32_t to)
 {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(to)
-                 : "memory");
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(to) : "memory");
 }
 
 // A pointer that is the same in all lanes, in scalar registers.
