@@ -66,3 +66,15 @@ def test_gemm_a8_fp32_keeps_small_products_beside_large(awq, M, out, n):
     want = torch.from_numpy(ex.sums(mx.dequantize(xc, xs), mx4.dequantize(c, s))).float()
     say("wrong", float((Y != want).float().mean()))
     assert torch.equal(Y, want)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_gemm_a8_small_tiles_with_weights_beyond_32_bits(awq, dt):
+    """32 tokens take the small tiles; the last rows against a call on those alone."""
+    say("small tiles beyond 2^32 bytes", dt)
+    M, out, n, last = 32, 540672, 16384, 32768
+    c, s, xc, xs = (torch.randint(lo, hi, shape, dtype=torch.uint8, device="cuda") for lo, hi, shape in
+                    [(0, 256, (out, n // 2)), (112, 120, (out, n // 32)), (0, 127, (M, n)), (112, 120, (M, n // 32))])
+    Y = awq.mx4_gemm_a8(xc, xs, c, s, dtype=DT[dt])
+    Z = awq.mx4_gemm_a8(xc, xs, c[-last:].contiguous(), s[-last:].contiguous(), dtype=DT[dt])
+    assert torch.equal(Y[:, -last:], Z) and bool(torch.isfinite(Z).all()) and bool((Z != 0).any())
