@@ -10,8 +10,9 @@
 // experts, go unsorted, in two launches.
 // (us: 1 token, 8 of 64 experts of 2048x1024 17; 8, 2 of 8 of 4096x14336 164, bound by the
 // weights of the seven that are hit, 4.0 TB/s; 203, 4 of 48 of 1056x1408 69: sort 5, up 39,
-// down 20, sum 5; 2048, 8 of 64 of 2048x1024 276: sort 11, up 174, down 63, sum 28 for 134 MB
-// of fp32 each way.)
+// down 20, sum 5; 2048, 8 of 64 of 2048x1024 267-288: sort 11, up 145-166, down 62, sum 29 for 134 MB
+// of fp32 each way. One block sorts: 16384 pairs, which its registers hold, 10.6; 16392 17;
+// 32768 32; 131072 119 of 1700; 2^20, of experts of 256x128, 1290 of 3130.)
 #include "mx8_stream.h"
 #include "mx8_tile.h"
 
@@ -546,9 +547,11 @@ hipError_t launch_mx4_experts(const uint8_t *xc, const uint8_t *xs, int64_t M, i
     float *const part = (float *)(base + l.part_off);
     const int64_t pairs = M * top_k, hit = pairs < experts ? pairs : experts;
     if (pairs <= (inter >= 4096 ? kDirect / 2 : kDirect)) {
-        // Two launches instead of four (1 token, 8 of 64 experts of 2048x1024 17 us, sorted 25;
-        // 2 tokens 22, 29). Long streams of many pairs hide the sort: 2 of 8 experts of
-        // 4096x14336, 1 token 44, sorted 47; 4 tokens 126, 126; 8 tokens 176, 164.
+        // Two launches instead of four (us unsorted and sorted, 1 token, 8 of 64 experts of
+        // 2048x1024 17, 25; 2 tokens 23, 29; 8 of 16 experts with hidden 4096, 1 token and 2: inter 2048
+        // 33, 40 and 57, 64; inter 4096 57, 66 and 95, 105, where the rule is early; inter 8192 105, 110 and
+        // 179, 170). Long streams of many pairs hide the sort: 2 of 8 experts of
+        // 4096x14336, 1 token 44, 47; 4 tokens 126, 126; 8 tokens 176, 164.
         k_experts_up<2, true><<<experts_grid<1>(pairs, inter / 32), 512, 0, st>>>(
             xc, xs, top_k, hidden / 32, inter, ids, (int)pairs, experts, nullptr, nullptr, nullptr, gu, gus, hc, hs);
         auto down = [&](auto *y) {
@@ -566,7 +569,8 @@ hipError_t launch_mx4_experts(const uint8_t *xc, const uint8_t *xs, int64_t M, i
     // Large tiles from 24 pairs an expert on (us by tiles and by streams, 8 of 64 experts of
     // 2048x1024: 64 tokens, 8 pairs an expert, 102, 78; 100 tokens 103, 83; 150 tokens, 19 pairs,
     // 104, 98; 200 tokens, 25 pairs, 105, 112; 300 tokens 104, 142; 4 of 48 of 1056x1408, which
-    // would rather have it later: 17 pairs an expert 104, 69; 25 pairs 105, 83; 33 pairs 106, 94)
+    // would rather have it later: 17 pairs an expert 104, 69; 25 pairs 105, 83; 33 pairs 106, 94).
+    // The host does not know how many experts are hit: few of many with all pairs stream.
     if (pairs >= 24 * (int64_t)experts) {
         const int64_t most = pairs / 256 + hit;
         k_experts_sort<true><<<1, 1024, 0, st>>>(ids, pairs, experts, list, place, count, tiles);
@@ -585,8 +589,9 @@ hipError_t launch_mx4_experts(const uint8_t *xc, const uint8_t *xs, int64_t M, i
         k_experts_sort<false><<<1, 1024, 0, st>>>(ids, pairs, experts, list, place, count, tiles);
         k_experts_up<1, false><<<experts_grid<1>(most, tiles_of(inter, 64)), 512, 0, st>>>(
             xc, xs, top_k, hidden / 32, inter, ids, (int)pairs, experts, list, count, tiles, gu, gus, hc, hs);
-        // (203 tokens, 4 of 48 experts of 1056x1408, by one, two, four waves a row tile: 71, 69,
-        // 70 us a layer; 64, 8 of 64 of 2048x1024 80, 77, 89; 8, 2 of 8 of 4096x14336 162, 167, 140)
+        // (us a layer by one, two, four waves a row tile: 203 tokens, 4 of 48 experts of 1056x1408 72,
+        // 69.5, 71; 64, 8 of 64 of 2048x1024 78.5, 78.5, 88; 16, 4 of 16 of 4096x2048 68, 68, 70, of
+        // 4096x8192 205, 199, 201; 8, 2 of 8 of 4096x14336 163, 166, 164)
         auto down = [&]<int S, bool EXACT>() {
             k_experts_down<S, EXACT><<<experts_grid<1>(most, tiles_of(hidden, 128 / S)), 512, 0, st>>>(
                 hc, hs, inter / 32, hidden, count, tiles, dn, dns, part);

@@ -14,8 +14,9 @@ namespace {
 template <typename TY> constexpr bool kExact = std::is_same<TY, float>::value;
 
 // Up to 16 tokens (see mx8_stream.h). Block: 8 / S row tiles of 16, S waves a tile. Bound by
-// the weights on their way, 4 KB a wave: 4 tokens x 28672x4096 17.9 us, 3.5 TB/s; small
-// layers by latency (1 token x 4096x4096 5.2 us, of which a launch is 2-3).
+// the latency of a wave's weights, of which it has one item of 4 KB on its way at a time (64 KB a
+// unit) and four in turn: 4 tokens x 28672x4096 17.9 us, 3.5 TB/s, fp32 Y 18.5; small
+// layers by that of a launch too (1 token x 4096x4096 5.2 us, of which a launch is 2-3).
 template <typename TY, int S>
 __global__ __launch_bounds__(512, 4) void k_mx8_gemm_stream(const uint8_t *__restrict__ xcodes,
                                                             const uint8_t *__restrict__ xscales, int M, int nb,
@@ -44,7 +45,8 @@ __global__ __launch_bounds__(512, 4) void k_mx8_gemm_stream(const uint8_t *__res
 
 // Few tokens or few tiles (see mx8_mid.h): 32 x 32 NT. Bound by what a unit's load path takes
 // (64 bytes a cycle, half of it for the weights' 64-byte rows) and by each wave's chain of
-// wait, LDS reads and products: 64 tokens x 4096x4096 8.3 us, 256 tokens 15 us, 570 TFLOP/s.
+// wait, LDS reads and products: 64 tokens x 4096x4096 8.3 us, 256 tokens 15 us, 570 TFLOP/s, fp32 Y
+// 9.5 and 16.8.
 template <typename TY, int NT>
 __global__ __launch_bounds__(kMidThreads) void k_mx8_gemm_mid(const uint8_t *__restrict__ xcodes,
                                                               const uint8_t *__restrict__ xscales, int64_t M, int nb,
@@ -76,7 +78,8 @@ __global__ __launch_bounds__(kMidThreads) void k_mx8_gemm_mid(const uint8_t *__r
 
 // Many tokens: tiles of 256 x 256 (see mx8_tile.h), those of a last round that fills at
 // most half of the chip cut in two. Bound by the matrix cores (60 % busy) and the loads that
-// their phases wait for: 2048 tokens x 28672x4096 203 us, 2370 TFLOP/s, 8192 tokens 2510.
+// their phases wait for: 2048 tokens x 28672x4096 203 us, 2370 TFLOP/s, 8192 tokens 2510; with
+// an fp32 Y, twice the matrix instructions, 366 us.
 template <typename TY, int MT>
 __device__ __forceinline__ void tile(Tile8<MT> &lds, int64_t m0, int64_t n0, const uint8_t *xcodes,
                                      const uint8_t *xscales, int64_t M, int nb, const uint8_t *codes,

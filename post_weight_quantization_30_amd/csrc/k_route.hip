@@ -6,9 +6,10 @@
 //
 // A wave a token; expert e is register e / 64 of lane e % 64. Scores in 64 bits: the
 // choice goes by differences that 32 bits lose (a sigmoid near 1, a bias much larger
-// than the score), and 256 exponentials a token cost less than the launch. Bound by the
-// issue of vector instructions, some 1000 a wave of 256 experts in 8 groups: 8192 tokens
-// 20.4 us (without groups 15.1, with one choice 10.8; 64 experts 8.8); 33 tokens of 48 3.5.
+// than the score). Bound by the issue of vector instructions, some 1000 a wave of 256
+// experts in 8 groups: 8192 tokens 20.4 us, about half of it for the scores (64-bit exponentials
+// and divisions of every expert) and half for the rounds of maxima (without groups 15.1, with
+// one choice 10.8; 64 experts 8.8). 33 tokens of 48 3.5, a launch.
 #include "awq_internal.h"
 
 namespace awq {
