@@ -38,6 +38,26 @@ def test_experts_sums(awq, case, dt):
     assert off <= 1
 
 
+# where a way ends and the next begins: 8, 16 and 17 pairs, 24 an expert, whole and half tiles; the sort's
+# second way (more than 16384 pairs)
+BORDERS = [(M, E, k, H, I) for M, E, k in [(8, 6, 1), (9, 6, 1), (16, 6, 1), (17, 6, 1), (4, 9, 5), (71, 6, 2), (72, 6, 2), (23, 1, 1), (24, 1, 1),
+                                           (128, 1, 1), (129, 1, 1), (256, 1, 1), (257, 1, 1), (385, 1, 1)]
+           for H, I in [(96, 4128), (4128, 96)]] + [(5500, 5, 3, 64, 96), (8200, 3, 2, 96, 64)]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("case", range(len(BORDERS)))
+def test_experts_where_ways_meet(awq, case, dt):
+    say("experts, borders of the ways", *BORDERS[case], dt)
+    some = ex.some_tokens(BORDERS[case][0], 4)
+    for show in (True, False):
+        layer = ex.Layer(*BORDERS[case], 200 + case, show)
+        Y = awq.mx4_experts(*dev(*layer.arrays()), dtype=DT[dt])
+        off = layer.check(Y.cpu().double().numpy(), dt, some)
+        say("err/bound", show, off)
+        assert off <= 1
+
+
 # M, out, in: up to 16 tokens by two, four, eight waves a row tile; small tiles; large ones, whole and half
 GEMM = [(1, 70, 32), (1, 300, 4096), (4, 20490, 160), (16, 10250, 608), (15, 1000, 14336), (17, 130, 1024), (33, 65, 32),
         (70, 500, 2080), (40, 2000, 4128), (128, 4100, 160), (250, 4090, 1184), (1000, 700, 1056), (2050, 4097, 256), (2050, 4097, 1312)]
